@@ -337,7 +337,8 @@ cudaError_t bdgemm64(const void* X, const void* W, void* Y, int nb, int64_t rows
 
 bool tc_split_supported(const Shape& s) {
   return s.nb1 == s.nb2 && s.in1 == 64 && s.out1 == 64 && s.in2 == 64 && s.out2 == 64 &&
-         s.nb1 >= 1 && s.nb1 <= 256;
+         s.nb1 >= 1 && s.nb1 <= 256 &&
+         s.nb1 % 8 == 0;  // the row permutations move 16-byte chunks of nb1 values
 }
 
 cudaError_t tc_split_fwd(const void* X, const void* R, const void* L, void* Y, const Shape& s,

@@ -223,3 +223,14 @@ def test_shape_beyond_every_kernel_is_unsupported_before_device_work():
 def test_oversized_dims_rejected():
     assert bdl.validate(dict(nb1=1 << 21, in1=1 << 20, out1=1, nb2=1, in2=1 << 21, out2=1), 1, "bf16") == \
         bdl.CODES["MONARCH_ERR_DIMS"]
+
+
+@pytest.mark.parametrize("nb", [1, 2, 4, 7, 12, 20])
+@pytest.mark.parametrize("transpose", [0, 1])
+def test_square_64_blocks_need_whole_permutation_chunks(nb, transpose):
+    """The 64 x 64-block passes permute rows in 16-byte chunks of nb values, so a block count that is
+    no multiple of 8 must run on another family (these read and wrote beyond their rows)."""
+    s = dict(nb1=nb, in1=64, out1=64, nb2=nb, in2=64, out2=64, out_transpose=transpose)
+    assert bdl.fwd_path(s) != 4
+    assert bdl.bwd_path(s) != 1
+    assert bdl.fwd_path(dict(s, nb1=8, nb2=8)) == 4 and bdl.bwd_path(dict(s, nb1=8, nb2=8)) == 1
