@@ -50,6 +50,9 @@ EXPORTED = (
     "monarch_linear_fwd", "monarch_linear_bwd", "monarch_project", "monarch_dyad_workspace_bytes",
     "monarch_dyad_path", "monarch_dyad_fwd", "monarch_dyad_bwd", "monarch_lattice_workspace_bytes",
     "monarch_lattice_path", "monarch_lattice_weight_elems", "monarch_lattice_fwd", "monarch_lattice_bwd",
+    "monarch_mx4_code_bytes", "monarch_mx4_scale_bytes", "monarch_mx4_quantise", "monarch_mx4_dequantise",
+    "monarch_mx4_linear_workspace_bytes", "monarch_mx4_linear_fwd", "monarch_mx4_linear_wfwd",
+    "monarch_mx4_linear_bwd", "monarch_mx4_fwd_workspace_bytes", "monarch_mx4_fwd",
 )
 
 
@@ -98,6 +101,29 @@ class MonarchLatticeDims(ctypes.Structure):
         ("naxes", ctypes.c_int32),
         ("n_in", ctypes.c_int32 * 4),
         ("n_out", ctypes.c_int32 * 4),
+        ("dtype", ctypes.c_int32),
+    ]
+
+
+class MonarchMx4Dims(ctypes.Structure):
+    """Mirror of ``monarch_mx4_dims`` in include/monarch.h."""
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("nblocks", ctypes.c_int32),
+        ("cols", ctypes.c_int32),
+        ("by_block", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+    ]
+
+
+class MonarchMx4LinearDims(ctypes.Structure):
+    """Mirror of ``monarch_mx4_linear_dims`` in include/monarch.h."""
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("nblocks", ctypes.c_int32),
+        ("in_blk", ctypes.c_int32),
+        ("out_blk", ctypes.c_int32),
+        ("has_bias", ctypes.c_int32),
         ("dtype", ctypes.c_int32),
     ]
 
@@ -179,6 +205,18 @@ def lib() -> ctypes.CDLL:
         L.monarch_lattice_fwd.restype = ctypes.c_int
         L.monarch_lattice_bwd.argtypes = [vp, vp, pp, tp, vp, pp, vp, ctypes.c_size_t, vp]
         L.monarch_lattice_bwd.restype = ctypes.c_int
+        qp, mp, sz = ctypes.POINTER(MonarchMx4Dims), ctypes.POINTER(MonarchMx4LinearDims), ctypes.c_size_t
+        for name, args, res in (
+                ("monarch_mx4_code_bytes", [qp], sz), ("monarch_mx4_scale_bytes", [qp], sz),
+                ("monarch_mx4_quantise", [vp, qp, vp, vp, vp], ctypes.c_int),
+                ("monarch_mx4_dequantise", [vp, vp, qp, vp, vp], ctypes.c_int),
+                ("monarch_mx4_linear_workspace_bytes", [mp], sz),
+                ("monarch_mx4_linear_fwd", [vp, vp, vp, vp, vp, mp, vp, vp], ctypes.c_int),
+                ("monarch_mx4_linear_wfwd", [vp, vp, vp, vp, mp, vp, vp, sz, vp], ctypes.c_int),
+                ("monarch_mx4_linear_bwd", [vp, vp, vp, vp, vp, mp, vp, vp, vp, vp, sz, vp], ctypes.c_int),
+                ("monarch_mx4_fwd_workspace_bytes", [dp], sz),
+                ("monarch_mx4_fwd", [vp, vp, vp, vp, vp, dp, vp, vp, sz, vp], ctypes.c_int)):
+            getattr(L, name).argtypes, getattr(L, name).restype = args, res
         for name in ("monarch_validate", "monarch_fwd", "monarch_bwd", "monarch_materialise",
                      "monarch_last_device_status", "monarch_debug_wait_timeout",
                      "monarch_fwd_path", "monarch_bwd_path", "monarch_bwd_noalloc"):
@@ -670,3 +708,17 @@ def kernel_launches() -> int:
 
 def status_string(code: int) -> str:
     return lib().monarch_status_string(int(code)).decode()
+
+
+# ---------------------------------------------------------------- microscaled 4-bit (MX4)
+_MX4 = ("Mx4", "mx4_quantise", "mx4_dequantise", "mx4_linear_fwd", "mx4_linear_bwd", "mx4_linear_workspace_bytes", "mx4_fwd")
+
+
+def __getattr__(name: str):
+    """The MX4 operators live in a module of their own, imported at first use (it needs torch)."""
+    if name in _MX4:
+        from . import mx4
+        for n in _MX4:
+            globals()[n] = getattr(mx4, n)
+        return globals()[name]
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))

@@ -1,0 +1,135 @@
+// Microscaled 4-bit (MX4) tensors: layout, element conversions and the launchers of mx4*.cu.
+//
+// A tensor of nblocks matrices of (rows, cols) is cut along cols into scale blocks of 32 (zeros
+// behind the end of a row).  Every value is an E2M1 code (0, .5, 1, 1.5, 2, 3, 4, 6 and a sign
+// bit) times its block's scale 2^(byte - 127) (E8M0; byte 255 stands for NaN).
+//   codes   [nblocks][rows][ceil(cols / 32) * 16] bytes, element 2i in the low half of byte i
+//   scales  [nblocks][ceil(rows / 128)][ceil(cols / 128)][512] bytes: the 128 rows x 4 scale blocks
+//           of a tile at (row % 32) * 16 + (row % 128) / 32 * 4 + block % 4, which is the order a
+//           tcgen05.cp of 32 lanes x 128 bits wants; rows and blocks behind the end hold byte 0.
+#pragma once
+
+#include "common.cuh"
+#include "ptx.cuh"
+
+namespace monarch {
+
+struct Mx4Shape {
+  int64_t rows;
+  int nblocks, cols;
+  __host__ __device__ int kblocks() const { return (cols + 31) / 32; }         // scale blocks of a row
+  __host__ __device__ int pitch() const { return kblocks() * 16; }             // bytes of a row's codes
+  __host__ __device__ int katoms() const { return (cols + 127) / 128; }        // scale tiles along a row
+  __host__ __device__ int64_t ratoms() const { return (rows + 127) / 128; }    // scale tiles along the rows
+  __host__ __device__ int64_t code_bytes() const { return (int64_t)nblocks * rows * pitch(); }
+  __host__ __device__ int64_t scale_bytes() const { return (int64_t)nblocks * ratoms() * katoms() * 512; }
+  __host__ __device__ int64_t code_row(int b, int64_t r) const { return ((int64_t)b * rows + r) * pitch(); }
+  // offset of the scale byte of (block b, row r, scale block kb)
+  __host__ __device__ int64_t scale_at(int b, int64_t r, int kb) const {
+    return ((((int64_t)b * ratoms() + (r >> 7)) * katoms() + (kb >> 2)) << 9) +
+           ((r & 31) << 4) + (((r >> 5) & 3) << 2) + (kb & 3);
+  }
+};
+
+struct Mx4View {  // codes and scales of one tensor
+  const uint8_t* codes;
+  const uint8_t* scales;
+  Mx4Shape s;
+};
+
+namespace mx4 {
+
+// One element in fp32.  A plain load: the header's __ldg of a bf16 is an assembly statement that the
+// compiler takes to have no effects, and it may then be issued ahead of the bounds test before it.
+__device__ __forceinline__ float load(const float* p) { return *p; }
+__device__ __forceinline__ float load(const __nv_bfloat16* p) {
+  return __uint_as_float((uint32_t)*(const uint16_t*)p << 16);
+}
+
+// Scale byte of a block whose largest magnitude has these fp32 bits (sign cleared):
+// floor(log2(amax)) - 2 + 127, not below 0; 255 for a block with an infinity or a NaN.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
+  const int e = (int)(amax_bits >> 23);
+  return e == 255 ? 255u : (uint32_t)(e > 2 ? e - 2 : 0);
+}
+// 2^(127 - byte): what a block's values are multiplied by before they are rounded.  Exact for
+// byte 0 .. 252; the NaN byte gives 0 (its codes carry nothing).
+__device__ __forceinline__ float inv_scale(uint32_t byte) {
+  return byte == 255 ? 0.f : __uint_as_float((254u - byte) << 23);
+}
+// 2^(byte - 127), a subnormal for byte 0.
+__device__ __forceinline__ float scale_value(uint32_t byte) {
+  return __uint_as_float(byte == 0 ? 0x00400000u : byte == 255 ? 0x7fc00000u : byte << 23);
+}
+// Eight values to codes (v[0] in the lowest four bits): nearest, ties to the even code, cut at 6.
+__device__ __forceinline__ uint32_t encode8(const float (&v)[8]) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return r;
+}
+// Value of one code without its scale.
+__device__ __forceinline__ float decode(uint32_t code) {
+  const uint32_t m = code & 7u;
+  const float a = m < 2 ? 0.5f * (float)m : __uint_as_float(((126u + (m >> 1)) << 23) | ((m & 1u) << 22));
+  return (code & 8u) ? -a : a;
+}
+// Eight codes to bf16 pairs without their scale, divided by 2^126: the E2M1 exponent and mantissa
+// bits land on the bf16 ones, so that one multiplication by a power of two finishes the job (a code
+// of 0.5 is a bf16 subnormal here and becomes a normal number by it).  p[i] holds codes 2i, 2i + 1.
+__device__ __forceinline__ void spread8(uint32_t w, uint32_t (&p)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // codes 2i and 2i+1 sit in bits 8i .. 8i+3 and 8i+4 .. 8i+7
+    const uint32_t c = w >> (8 * i);
+    const uint32_t lo = c & 15u, hi = (c >> 4) & 15u;
+    p[i] = ((lo & 8u) << 12) | ((lo & 7u) << 6) | ((hi & 8u) << 28) | ((hi & 7u) << 22);
+  }
+}
+
+}  // namespace mx4
+
+// ---- launchers (cudaError_t; arguments already checked) ----
+// by_block: X is (nblocks, rows, cols); otherwise (rows, nblocks * cols).
+cudaError_t mx4_quantise(const void* X, const Mx4Shape& s, bool by_block, int dtype, uint8_t* codes, uint8_t* scales,
+                         cudaStream_t st);
+cudaError_t mx4_dequantise(const Mx4View& q, bool by_block, int dtype, void* X, cudaStream_t st);
+
+// Where result (block b, row m, column n) of a product goes.
+struct Mx4Out {
+  int64_t b, m, n;  // strides in elements
+  __host__ __device__ int64_t at(int64_t blk, int64_t row, int64_t col) const { return blk * b + row * m + col * n; }
+  // (rows, nb * out)
+  static Mx4Out blocks(int64_t nb, int64_t out) { return Mx4Out{out, nb * out, 1}; }
+  // the same with a block's results nb apart: column n of block b at n * nb + b
+  static Mx4Out transposed(int64_t nb, int64_t out) { return Mx4Out{1, nb * out, nb}; }
+};
+
+struct Mx4Linear {
+  int64_t rows;
+  int nb, in, out;
+  bool has_bias;
+  int dtype;
+  Mx4Shape x() const { return Mx4Shape{rows, nb, in}; }
+  Mx4Shape w() const { return Mx4Shape{out, nb, in}; }
+};
+// Tiled FMA kernels for every size and type (mx4_generic.cu).
+cudaError_t mx4_generic_fwd(const Mx4View& x, const Mx4View& w, const void* bias, const Mx4Linear& d, void* Y,
+                            cudaStream_t st);
+// X (rows, nb * in) as it is; X and Y may differ in type (bias has Y's).
+cudaError_t mx4_generic_wfwd(const void* X, int x_dtype, const Mx4View& w, const void* bias, int64_t rows, const Mx4Out& o,
+                             void* Y, int y_dtype, cudaStream_t st);
+cudaError_t mx4_generic_bwd_x(const void* dY, const Mx4View& w, const Mx4Linear& d, void* dX, cudaStream_t st);
+cudaError_t mx4_generic_bwd_w(const void* dY, const Mx4View& x, const Mx4Linear& d, void* dW, cudaStream_t st);
+// dbias[c] = sum over rows of dY[r][c], rows in a fixed order; part: mx4_dbias_bytes of scratch.
+size_t mx4_dbias_bytes(int64_t rows, int64_t cols);
+cudaError_t mx4_dbias(const void* dY, int64_t rows, int64_t cols, int dtype, float* part, void* dbias,
+                      cudaStream_t st);
+
+}  // namespace monarch

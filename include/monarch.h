@@ -337,6 +337,79 @@ MONARCH_API int monarch_lattice_bwd(const void* dY, const void* X, const void* c
                                     const monarch_lattice_dims* ld, void* dX, void* const* dW, void* workspace,
                                     size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------- microscaled 4-bit (MX4)
+ * Block-diagonal weights and activations in 4 bits (OCP Microscaling Formats specification,
+ * MXFP4): along the inner axis of a product every 32 values share one power-of-two scale and each
+ * is an E2M1 code,
+ *   e = floor(log2(max |v|)) - 2, not below -127;  scale byte e + 127 (E8M0)
+ *   code = v / 2^e rounded to the nearest of 0, .5, 1, 1.5, 2, 3, 4, 6 (ties to the even code),
+ *          cut at 6, with v's sign.
+ * A block of zeros has scale byte 0; a block that holds an infinity or a NaN has byte 255 and
+ * stands for 32 NaNs.  Values of a row's last block behind `cols` are zeros.
+ *
+ * A quantised tensor is two caller-owned buffers, 16-byte aligned:
+ *   codes   [nblocks][rows][ceil(cols / 32) * 16] bytes, element 2i in the low half of byte i
+ *   scales  [nblocks][ceil(rows / 128)][ceil(cols / 128)][512] bytes, the scale of (row, 32-block k)
+ *           of a tile at (row % 32) * 16 + (row % 128) / 32 * 4 + k % 4; the rest of a tile is 0 */
+typedef struct {
+  int64_t rows;           /* rows of each block's matrix; 0 is a valid no-op            */
+  int32_t nblocks, cols;  /* blocks; columns of a block (the inner axis, quantised)     */
+  int32_t by_block;       /* plain tensor: 1: (nblocks, rows, cols), a weight;
+                             0: (rows, nblocks * cols), activations                     */
+  int32_t dtype;          /* monarch_dtype of the plain tensor                          */
+} monarch_mx4_dims;
+
+/* Bytes of the two buffers (0 if d is bad).  Host-only. */
+MONARCH_API size_t monarch_mx4_code_bytes(const monarch_mx4_dims* d);
+MONARCH_API size_t monarch_mx4_scale_bytes(const monarch_mx4_dims* d);
+/* X to codes and scales, and their values back (exact in both types).  d->dtype may differ between
+ * the two calls.  MONARCH_ERR_UNSUPPORTED beyond 2^20 columns, 65535 blocks, 2^22 columns in all or
+ * 2^31 - 256 rows. */
+MONARCH_API int monarch_mx4_quantise(const void* X, const monarch_mx4_dims* d, void* codes, void* scales,
+                                     void* stream);
+MONARCH_API int monarch_mx4_dequantise(const void* codes, const void* scales, const monarch_mx4_dims* d, void* X,
+                                       void* stream);
+
+/* Block-diagonal linear layer with MX4 operands (nblocks = 1: a dense layer).  X^ and W^ stand for the
+ * values of the quantised X (rows, nblocks * in_blk) and W (nblocks, out_blk, in_blk):
+ *   Y[r][b*out_blk + o] = sum_i X^[r][b*in_blk + i] W^[b][o][i] (+ bias[b*out_blk + o]).
+ * Products are exact, sums fp32, Y rounded once. */
+typedef struct {
+  int64_t rows;
+  int32_t nblocks, in_blk, out_blk;
+  int32_t has_bias;       /* 1: bias / dbias (nblocks * out_blk) are used               */
+  int32_t dtype;          /* monarch_dtype of X, bias, Y and the gradients              */
+} monarch_mx4_linear_dims;
+
+/* Workspace of monarch_mx4_linear_wfwd and _bwd, 256-byte aligned (0: may be NULL; 0 if ld is bad). */
+MONARCH_API size_t monarch_mx4_linear_workspace_bytes(const monarch_mx4_linear_dims* ld);
+/* Both operands in MX4. */
+MONARCH_API int monarch_mx4_linear_fwd(const void* x_codes, const void* x_scales, const void* w_codes,
+                                       const void* w_scales, const void* bias, const monarch_mx4_linear_dims* ld,
+                                       void* Y, void* stream);
+/* X as it is (rows, nblocks * in_blk), W in MX4: serving, from one token upwards. */
+MONARCH_API int monarch_mx4_linear_wfwd(const void* X, const void* w_codes, const void* w_scales, const void* bias,
+                                        const monarch_mx4_linear_dims* ld, void* Y, void* workspace,
+                                        size_t workspace_bytes, void* stream);
+/* Gradients of monarch_mx4_linear_fwd for its quantised operands and the upstream gradient dY (a
+ * training step passes them on to the unquantised ones):
+ *   dX[r][b*in_blk + i] = sum_o dY[r][b*out_blk + o] W^[b][o][i]
+ *   dW[b][o][i]         = sum_r dY[r][b*out_blk + o] X^[r][b*in_blk + i]
+ *   dbias[c]            = sum_r dY[r][c]                       (has_bias)
+ * all overwritten, rows summed in a fixed order.  dX or dW may be NULL (not wanted); then the operand
+ * that only it reads (W; X) may be NULL too, as for a frozen layer. */
+MONARCH_API int monarch_mx4_linear_bwd(const void* dY, const void* x_codes, const void* x_scales, const void* w_codes,
+                                       const void* w_scales, const monarch_mx4_linear_dims* ld, void* dX, void* dW,
+                                       void* dbias, void* workspace, size_t workspace_bytes, void* stream);
+
+/* monarch_fwd with both factors in MX4: R as (nb1, out1, in1), L as (nb2, out2, in2), quantised by block.
+ * X and Y have d->dtype.  Up to 64 rows (decoding) the middle vector stays in fp32; longer batches run
+ * monarch_fwd's kernels on the factors' values, with its rounding of the middle vector.  workspace: >= monarch_mx4_fwd_workspace_bytes(d), 256-byte aligned. */
+MONARCH_API size_t monarch_mx4_fwd_workspace_bytes(const monarch_dims* d);
+MONARCH_API int monarch_mx4_fwd(const void* X, const void* r_codes, const void* r_scales, const void* l_codes,
+                                const void* l_scales, const monarch_dims* d, void* Y, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
 /* Number of kernels this library has launched in this process (every device and
  * stream), counted on the host at each successful launch.  Host-only; a caller
  * reads it before and after a region to count that region's launches. */

@@ -376,3 +376,67 @@ def lattice_backward(n_in: list, n_out: list, Ws: list, X, dY):
         dAt = np.einsum("rlo,loi->rli", Gt, W)
         G = np.moveaxis(dAt.reshape([rows] + [cin[s] for s in others] + [cin[t]]), -1, 1 + t)
     return np.ascontiguousarray(G.reshape(rows, -1)), dWs
+
+
+# ---------------------------------------------------------------- microscaled 4-bit (MX4)
+MX4_GRID = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+
+
+def mx4_encode(x: np.ndarray):
+    """(codes 0..15, scale bytes) of x along its last axis, in blocks of 32 with zeros behind the end:
+    codes (..., kblocks, 32), bytes (..., kblocks).  OCP Microscaling Formats, MXFP4."""
+    x = np.asarray(x, dtype=np.float64)
+    n = x.shape[-1]
+    v = np.concatenate([x, np.zeros(x.shape[:-1] + (-n % 32,))], axis=-1).reshape(x.shape[:-1] + (-(-n // 32), 32))
+    top = np.abs(v).max(axis=-1)
+    bad = ~np.isfinite(v).all(axis=-1)
+    e = np.where((top > 0) & ~bad, np.frexp(np.where(bad, 1.0, top))[1] - 3, -127).clip(-127, 125)
+    a = np.where(bad[..., None], 0.0, np.abs(np.where(bad[..., None], 0.0, v)) / np.exp2(e.astype(np.float64))[..., None])
+    dist = np.abs(a[..., None] - MX4_GRID)
+    first = np.argmin(dist, axis=-1)
+    tie = (dist == dist.min(axis=-1, keepdims=True)).sum(axis=-1) == 2  # halfway between first and first + 1
+    codes = first + (tie & (first % 2 == 1))
+    codes = codes + np.where(np.signbit(v) & ~bad[..., None], 8, 0)
+    return codes.astype(np.uint8), np.where(bad, 255, e + 127).astype(np.uint8)
+
+
+def mx4_decode(codes: np.ndarray, scales: np.ndarray, n: int) -> np.ndarray:
+    """float64 values of mx4_encode's result, cut to n columns."""
+    v = MX4_GRID[codes & 7] * np.where(codes & 8, -1.0, 1.0)
+    s = np.where(scales == 255, np.nan, np.exp2(scales.astype(np.float64) - 127))
+    v = v * s[..., None]
+    return v.reshape(v.shape[:-2] + (v.shape[-2] * 32,))[..., :n]
+
+
+def mx4_round(x: np.ndarray) -> np.ndarray:
+    """x rounded to MX4 along its last axis."""
+    return mx4_decode(*mx4_encode(x), np.asarray(x).shape[-1])
+
+
+def mx4_buffers(x: np.ndarray):
+    """The code and scale buffers of x (nblocks, rows, cols), laid out as include/monarch.h says."""
+    nb, rows, cols = x.shape
+    codes, scales = mx4_encode(x)
+    flat = codes.reshape(nb, rows, codes.shape[-2] * 32)
+    packed = flat[..., 0::2] | (flat[..., 1::2] << 4)
+    out = np.zeros((nb, -(-rows // 128), -(-cols // 128), 512), dtype=np.uint8)
+    for r in range(rows):
+        for k in range(scales.shape[-1]):
+            out[:, r // 128, k // 4, (r % 32) * 16 + (r % 128) // 32 * 4 + k % 4] = scales[:, r, k]
+    return packed, out
+
+
+def mx4_linear_forward(X: np.ndarray, W: np.ndarray, bias=None) -> np.ndarray:
+    """Y (rows, nb*out) = X (rows, nb*in) times the blocks of W (nb, out, in), given as values."""
+    nb, out, inn = W.shape
+    Y = np.einsum("rki,koi->rko", X.reshape(X.shape[0], nb, inn), W, optimize=True).reshape(X.shape[0], nb * out)
+    return Y if bias is None else Y + bias
+
+
+def mx4_linear_backward(dY: np.ndarray, X: np.ndarray, W: np.ndarray):
+    """(dX, dW, dbias) of mx4_linear_forward."""
+    nb, out, inn = W.shape
+    rows = dY.shape[0]
+    d3, x3 = dY.reshape(rows, nb, out), X.reshape(rows, nb, inn)
+    return (np.einsum("rko,koi->rki", d3, W, optimize=True).reshape(rows, nb * inn),
+            np.einsum("rko,rki->koi", d3, x3, optimize=True), dY.sum(axis=0))

@@ -1,0 +1,453 @@
+"""MX4 operators on the GPU against the float64 oracle.
+
+Rounding to MX4 is exact arithmetic (a power-of-two scale, one rounding), so codes, scales and values
+are compared for equality.  Products are compared element by element with
+    |Y - ref| <= half * |ref| + terms * 2^-23 * sum |factors|  (+ the smallest normal number),
+where half is the result type's half step (2^-8 bf16, 2^-24 fp32) and `terms` the length of the sum:
+each of its fp32 additions is off by at most 2^-23 of a partial sum (2^-24 if it rounds, twice that if
+it cuts off), and no partial sum exceeds the sum of the magnitudes.
+"""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import block_diagonal_linear_b200 as bdl
+import oracle
+
+pytestmark = pytest.mark.gpu
+
+HALF = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}
+TORCH = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def dev(a, dtype):
+    """A float64 array on the GPU in `dtype`, and the values it has there."""
+    t = torch.from_numpy(np.ascontiguousarray(a, dtype=np.float64)).to(TORCH[dtype]).cuda()
+    return t, f64(t)
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def close(got, ref, mags, terms, dtype, what, extra=0.0):
+    g = f64(got)
+    assert g.shape == ref.shape
+    tol = HALF[dtype] * np.abs(ref) + (terms * 2.0 ** -23) * mags + 2.0 ** -126 + extra
+    bad = ~(np.abs(g - ref) <= tol)
+    assert not bad.any(), "%s: %d of %d off, first %s: %r, want %r +- %r" % (
+        what, bad.sum(), bad.size, np.argwhere(bad)[0], g[bad][0], ref[bad][0], tol[bad][0])
+
+
+def hard_values(rng, shape):
+    """Values over the whole range of exponents: ties, cut values, zeros, subnormals."""
+    x = rng.standard_normal(shape) * np.exp2(rng.integers(-30, 30, shape[:-1] + (1,)))
+    kind = rng.integers(0, 8, shape)
+    x = np.where(kind == 0, 0.0, x)
+    x = np.where(kind == 1, -0.0, x)
+    steps = rng.choice([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0, 7.0, 7.75], shape) * rng.choice([-1, 1], shape)
+    return np.where(kind >= 5, steps * np.exp2(rng.integers(-3, 3, shape)), x)
+
+
+SIZES = [(1, 1, 1), (1, 1, 32), (1, 7, 33), (2, 3, 31), (3, 128, 128), (2, 129, 100), (1, 300, 1000), (5, 64, 4),
+         (1, 1, 4096), (4, 130, 264), (7, 65, 257)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("by_block", [True, False])
+@pytest.mark.parametrize("nb,rows,cols", SIZES)
+def test_quantise_equals_oracle(nb, rows, cols, by_block, dtype):
+    rng = np.random.default_rng(rows * 1000 + cols)
+    X = hard_values(rng, (nb, rows, cols))
+    t, v = dev(X if by_block else X.transpose(1, 0, 2).reshape(rows, nb * cols), dtype)
+    b = v if by_block else v.reshape(rows, nb, cols).transpose(1, 0, 2)
+    q = bdl.mx4_quantise(t) if by_block else bdl.mx4_quantise(t, nblocks=nb)
+    codes, scales = oracle.mx4_buffers(b)
+    assert np.array_equal(q.codes.cpu().numpy().reshape(codes.shape), codes)
+    assert np.array_equal(q.scales.cpu().numpy().reshape(scales.shape), scales)
+    want = oracle.mx4_round(b)
+    if not by_block:
+        want = want.transpose(1, 0, 2).reshape(rows, nb * cols)
+    for out in ("bf16", "f32"):
+        assert np.array_equal(f64(bdl.mx4_dequantise(q, out)), want)
+    assert bdl.mx4_dequantise(q).dtype == t.dtype
+
+
+def test_quantise_special_values():
+    """Subnormals, the largest finite values, and blocks with an infinity or a NaN."""
+    X = np.zeros((1, 8, 96))
+    X[0, 0, :4] = [2.0 ** -149, 2.0 ** -140, -2.0 ** -133, 2.0 ** -130]
+    X[0, 1, :3] = [2.0 ** -126, 2.0 ** -127, -3 * 2.0 ** -128]
+    X[0, 2, :3] = [3.3e38, -3e38, 1e38]
+    X[0, 3, :] = 1.0
+    X[0, 3, 40] = np.inf
+    X[0, 4, 7] = np.nan
+    X[0, 5, 95] = -np.inf
+    X[0, 6, 3] = 1e30
+    X[0, 6, 4] = 1e-30
+    for dtype in ("bf16", "f32"):
+        t, v = dev(X, dtype)
+        q = bdl.mx4_quantise(t)
+        codes, scales = oracle.mx4_buffers(v)
+        assert np.array_equal(q.codes.cpu().numpy().reshape(codes.shape), codes)
+        assert np.array_equal(q.scales.cpu().numpy().reshape(scales.shape), scales)
+        assert np.array_equal(f64(bdl.mx4_dequantise(q)), oracle.mx4_round(v), equal_nan=True)
+
+
+def test_quantised_again_is_the_same():
+    t, _ = dev(np.random.default_rng(3).standard_normal((40, 300)), "bf16")
+    once = bdl.mx4_dequantise(bdl.mx4_quantise(t, nblocks=3))
+    # a second rounding may only raise the scale's resolution, never move a value
+    assert torch.equal(once, bdl.mx4_dequantise(bdl.mx4_quantise(once, nblocks=3)))
+
+
+# ---------------------------------------------------------------- products
+def layer(rows, nb, inn, out, bias, dtype, seed=0):
+    """Device tensors of a layer and the float64 values that its quantised operands have."""
+    rng = np.random.default_rng(seed + 7 * rows + inn + out)
+    X = rng.standard_normal((rows, nb * inn)) * np.where(rng.random(nb * inn) < 0.05, 12.0, 1.0)
+    W = rng.uniform(-1, 1, (nb, out, inn)) / np.sqrt(inn)
+    t = {}
+    t["X"], x = dev(X, dtype)
+    t["W"], w = dev(W, dtype)
+    t["dY"], dy = dev(rng.standard_normal((rows, nb * out)), dtype)
+    t["b"], b = dev(rng.standard_normal(nb * out), dtype)
+    if not bias:
+        t["b"], b = None, None
+    xr = oracle.mx4_round(x.reshape(rows, nb, inn)).reshape(rows, nb * inn)
+    return t, dict(x=x, xr=xr, w=oracle.mx4_round(w), dy=dy, b=b)
+
+
+def check_forward(Y, x, v, inn, dtype, what):
+    ref = oracle.mx4_linear_forward(x, v["w"], v["b"])
+    mags = oracle.mx4_linear_forward(np.abs(x), np.abs(v["w"]), None if v["b"] is None else np.abs(v["b"]))
+    close(Y, ref, mags, inn + 2, dtype, what)
+
+
+LAYERS = [  # (rows, nblocks, in, out, bias)
+    (1, 1, 1, 1, True), (1, 1, 32, 8, False), (1, 4, 256, 1024, True), (2, 3, 200, 500, True), (5, 1, 33, 130, False),
+    (8, 2, 64, 64, False), (9, 1, 1000, 72, True), (33, 4, 250, 100, True), (64, 2, 512, 256, False),
+    (65, 1, 640, 96, True), (127, 2, 96, 200, True), (128, 1, 128, 128, False), (129, 2, 160, 192, True),
+    (200, 16, 48, 48, False), (300, 1, 2048, 384, True), (257, 3, 64, 320, True), (513, 1, 320, 129, False),
+    (700, 2, 256, 512, True), (1024, 1, 512, 1024, False),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,nb,inn,out,bias", LAYERS)
+def test_linear_forward_both_quantised(rows, nb, inn, out, bias, dtype):
+    t, v = layer(rows, nb, inn, out, bias, dtype)
+    Wq, Xq = bdl.mx4_quantise(t["W"]), bdl.mx4_quantise(t["X"], nblocks=nb)
+    Y = bdl.mx4_linear_fwd(Xq, Wq, bias=t["b"])
+    assert bdl.last_device_status() == 0
+    check_forward(Y, v["xr"], v, inn, dtype, "Y")
+    assert torch.equal(Y, bdl.mx4_linear_fwd(Xq, Wq, bias=t["b"]))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,nb,inn,out,bias", LAYERS)
+def test_linear_forward_weights_only(rows, nb, inn, out, bias, dtype):
+    t, v = layer(rows, nb, inn, out, bias, dtype, seed=1)
+    Wq = bdl.mx4_quantise(t["W"])
+    Y = bdl.mx4_linear_fwd(t["X"], Wq, bias=t["b"])
+    assert bdl.last_device_status() == 0
+    check_forward(Y, v["x"], v, inn, dtype, "Y")
+    assert torch.equal(Y, bdl.mx4_linear_fwd(t["X"], Wq, bias=t["b"]))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,nb,inn,out,bias", LAYERS)
+def test_linear_backward(rows, nb, inn, out, bias, dtype):
+    t, v = layer(rows, nb, inn, out, bias, dtype, seed=2)
+    Wq, Xq = bdl.mx4_quantise(t["W"]), bdl.mx4_quantise(t["X"], nblocks=nb)
+    got = bdl.mx4_linear_bwd(t["dY"], Xq, Wq, bias=bias)
+    assert bdl.last_device_status() == 0
+    ref = oracle.mx4_linear_backward(v["dy"], v["xr"], v["w"])
+    mags = oracle.mx4_linear_backward(np.abs(v["dy"]), np.abs(v["xr"]), np.abs(v["w"]))
+    for g, r, m, terms, what in zip(got, ref, mags, (out, rows, rows), ("dX", "dW", "dbias")):
+        if what == "dbias" and not bias:
+            assert g is None
+            continue
+        close(g, r, m, terms + 2, dtype, what)
+    again = bdl.mx4_linear_bwd(t["dY"], Xq, Wq, bias=bias)
+    assert all(torch.equal(a, b) for a, b in zip(got, again) if a is not None)
+    # the parts alone: a frozen layer's dX, and dW without dX
+    dX, dW, _ = bdl.mx4_linear_bwd(t["dY"], None, Wq)
+    assert dW is None and torch.equal(dX, got[0])
+    dX, dW, _ = bdl.mx4_linear_bwd(t["dY"], Xq, Wq, need_dX=False)
+    assert dX is None and torch.equal(dW, got[1])
+
+
+def test_backward_against_differences():
+    """A step in one coordinate of an fp32 operand, big enough to move its quantised value, moves
+    sum(Y * dY) by the gradient times that value's move (the layer is linear in each operand)."""
+    rng = np.random.default_rng(5)
+    rows, nb, inn, out = 6, 2, 40, 24
+    X, W = rng.standard_normal((rows, nb * inn)), rng.standard_normal((nb, out, inn))
+    t = {k: dev(a, "f32")[0] for k, a in (("X", X), ("W", W), ("dY", rng.standard_normal((rows, nb * out))))}
+    Wq, Xq = bdl.mx4_quantise(t["W"]), bdl.mx4_quantise(t["X"], nblocks=nb)
+    dX, dW, _ = bdl.mx4_linear_bwd(t["dY"], Xq, Wq)
+
+    def loss(Xq, Wq):
+        return float((bdl.mx4_linear_fwd(Xq, Wq, dtype="f32").double() * t["dY"].double()).sum())
+
+    base, xv, wv = loss(Xq, Wq), bdl.mx4_dequantise(Xq), bdl.mx4_dequantise(Wq)
+    for k in range(4):
+        i, j = int(rng.integers(rows)), int(rng.integers(nb * inn))
+        x2 = t["X"].clone()
+        x2[i, j] = -x2[i, j] + 0.3
+        q2 = bdl.mx4_quantise(x2, nblocks=nb)
+        move = (bdl.mx4_dequantise(q2) - xv).double()
+        assert abs(loss(q2, Wq) - base - float((dX.double() * move).sum())) < 1e-3
+        w2 = t["W"].clone()
+        w2[k % nb, i, j % inn] += 0.7
+        q2 = bdl.mx4_quantise(w2)
+        move = (bdl.mx4_dequantise(q2) - wv).double()
+        assert abs(loss(Xq, q2) - base - float((dW.double() * move).sum())) < 1e-3
+
+
+@pytest.mark.parametrize("rows,nb,inn,out", [(3, 2, 96, 80), (40, 2, 96, 80), (300, 2, 128, 192)])
+def test_nan_and_infinity_stay_in_their_rows(rows, nb, inn, out):
+    t, v = layer(rows, nb, inn, out, False, "bf16", seed=3)
+    X, W = t["X"].clone(), t["W"].clone()
+    X[1, inn + 5] = float("nan")     # row 1, block 1
+    X[2, 3] = float("inf")           # row 2, block 0
+    W[1, 7, 2] = float("inf")        # block 1, output 7
+    Xq, Wq = bdl.mx4_quantise(X, nblocks=nb), bdl.mx4_quantise(W)
+    bad = np.zeros((rows, nb, out), dtype=bool)
+    bad[1, 1, :] = bad[2, 0, :] = bad[:, 1, 7] = True
+    for Y in (bdl.mx4_linear_fwd(Xq, Wq), bdl.mx4_linear_fwd(X, Wq)):
+        y = f64(Y).reshape(rows, nb, out)
+        assert not np.isfinite(y[bad]).any()
+        assert np.isfinite(y[~bad]).all()
+    dX, dW, _ = bdl.mx4_linear_bwd(t["dY"], Xq, Wq)
+    bad_x = np.zeros((rows, nb, inn), dtype=bool)
+    bad_x[:, 1, :32] = True          # the NaN weight block's 32 inputs
+    assert np.array_equal(np.isnan(f64(dX).reshape(rows, nb, inn)), bad_x)
+    bad_w = np.zeros((nb, out, inn), dtype=bool)
+    bad_w[1, :, :32] = bad_w[0, :, :32] = True   # columns of the NaN activation blocks (5 and 3 are in block 0 of 32)
+    assert np.array_equal(np.isnan(f64(dW)), bad_w)
+
+
+def test_extreme_scales():
+    """Weights of 2^100 and 2^-100 against activations that bring the products back into range."""
+    rng = np.random.default_rng(9)
+    inn, out = 64, 40
+    for rows in (2, 150):
+        X = rng.standard_normal((rows, inn))
+        W = rng.standard_normal((1, out, inn))
+        X[:, :32] *= 2.0 ** -100
+        W[:, :, :32] *= 2.0 ** 100
+        X[:, 32:] *= 2.0 ** 90
+        W[:, :, 32:] *= 2.0 ** -90
+        for dtype in ("bf16", "f32"):
+            t, x = dev(X, dtype)
+            w, wv = dev(W, dtype)
+            v = dict(w=oracle.mx4_round(wv), b=None)
+            Wq = bdl.mx4_quantise(w)
+            check_forward(bdl.mx4_linear_fwd(t, Wq), x, v, inn, dtype, "weights only")
+            check_forward(bdl.mx4_linear_fwd(bdl.mx4_quantise(t), Wq), oracle.mx4_round(x), v, inn, dtype, "both")
+
+
+# ---------------------------------------------------------------- Monarch map
+MONARCH = [  # (rows, nb1, in1, out1, nb2, in2, out2, out_transpose)
+    (1, 4, 256, 256, 4, 256, 1024, 0), (3, 16, 16, 16, 16, 16, 16, 1), (1, 64, 64, 64, 64, 64, 64, 1),
+    (32, 32, 32, 32, 32, 32, 32, 1), (33, 16, 48, 48, 48, 16, 64, 1), (7, 4, 250, 250, 4, 250, 1000, 0),
+    (5, 3, 10, 8, 4, 6, 5, 1), (2, 1, 40, 24, 2, 12, 9, 0), (64, 4, 256, 64, 4, 64, 64, 0), (65, 8, 64, 64, 8, 64, 128, 0),
+    (200, 32, 32, 32, 32, 32, 32, 1), (300, 4, 256, 256, 4, 256, 1024, 0)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,nb1,in1,out1,nb2,in2,out2,tr", MONARCH)
+def test_monarch_forward(rows, nb1, in1, out1, nb2, in2, out2, tr, dtype):
+    shape = dict(nb1=nb1, in1=in1, out1=out1, nb2=nb2, in2=in2, out2=out2, out_transpose=tr)
+    rng = np.random.default_rng(rows + in1 + out2)
+    X, x = dev(rng.standard_normal((rows, nb1 * in1)), dtype)
+    R, r = dev(rng.uniform(-1, 1, (nb1, out1, in1)) / np.sqrt(in1), dtype)
+    L, l = dev(rng.uniform(-1, 1, (nb2, out2, in2)) / np.sqrt(in2), dtype)
+    Rq, Lq = bdl.mx4_quantise(R), bdl.mx4_quantise(L)
+    Y = bdl.mx4_fwd(X, Rq, Lq, shape)
+    assert bdl.last_device_status() == 0
+    r, l = oracle.mx4_round(r), oracle.mx4_round(l)
+    ref = oracle.forward(shape, x, r, l)
+    mags = oracle.forward(shape, np.abs(x), np.abs(r), np.abs(l))
+    # long batches hold the middle vector in the tensors' type: half a step of every middle value
+    middle = HALF[dtype] * 1.01 * oracle.forward(shape, np.abs(x), np.abs(r), np.abs(l))
+    close(Y, ref, mags, in1 + in2 + 4, dtype, "Y", extra=middle)
+    assert torch.equal(Y, bdl.mx4_fwd(X, Rq, Lq, shape))
+
+
+def test_monarch_few_tokens_keep_the_middle_vector():
+    """Up to 64 tokens the middle vector is not rounded to bf16: the result is half a step off."""
+    shape = dict(nb1=32, in1=32, out1=32, nb2=32, in2=32, out2=32, out_transpose=1)
+    rng = np.random.default_rng(1)
+    R, r = dev(rng.uniform(-1, 1, (32, 32, 32)), "bf16")
+    L, l = dev(rng.uniform(-1, 1, (32, 32, 32)), "bf16")
+    r, l = oracle.mx4_round(r), oracle.mx4_round(l)
+    for rows in (1, 4, 17, 64):
+        X, x = dev(rng.standard_normal((rows, 1024)), "bf16")
+        Y = bdl.mx4_fwd(X, bdl.mx4_quantise(R), bdl.mx4_quantise(L), shape)
+        mags = oracle.forward(shape, np.abs(x), np.abs(r), np.abs(l))
+        # the middle value may be split into two bf16 parts: 2^-16 of it is lost at most
+        close(Y, oracle.forward(shape, x, r, l), mags, 70, "bf16", "Y", extra=2.0 ** -16 * mags)
+
+
+# ---------------------------------------------------------------- as they are used
+def test_training_steps_of_a_quantised_layer():
+    """Forward, backward and update of fp32 master weights for three steps: every step's outputs are the
+    oracle's for that step's weights."""
+    rows, nb, inn, out = 150, 2, 128, 192
+    rng = np.random.default_rng(11)
+    W = torch.from_numpy(rng.uniform(-1, 1, (nb, out, inn)) / np.sqrt(inn)).float().cuda()
+    b = torch.zeros(nb * out, device="cuda")
+    for step in range(3):
+        X, x = dev(rng.standard_normal((rows, nb * inn)), "bf16")
+        T, target = dev(rng.standard_normal((rows, nb * out)), "bf16")
+        Wq, Xq = bdl.mx4_quantise(W), bdl.mx4_quantise(X, nblocks=nb)
+        bias, bv = dev(f64(b), "bf16")
+        Y = bdl.mx4_linear_fwd(Xq, Wq, bias=bias, dtype="bf16")
+        v = dict(w=oracle.mx4_round(f64(W)), b=bv)
+        xr = oracle.mx4_round(x.reshape(rows, nb, inn)).reshape(rows, -1)
+        check_forward(Y, xr, v, inn, "bf16", "Y")
+        dY = (Y - T) / rows
+        dX, dW, db = bdl.mx4_linear_bwd(dY, Xq, Wq, bias=True)
+        refs = oracle.mx4_linear_backward(f64(dY), xr, v["w"])
+        mags = oracle.mx4_linear_backward(np.abs(f64(dY)), np.abs(xr), np.abs(v["w"]))
+        for g, r, m, terms, what in zip((dX, dW, db), refs, mags, (out, rows, rows), ("dX", "dW", "db")):
+            close(g, r, m, terms + 2, "bf16", what)
+        W -= 0.5 * dW.float()
+        b -= 0.5 * db.float()
+    assert bdl.last_device_status() == 0
+
+
+def test_serving_chain_matches_its_parts():
+    """Prompt, then single tokens, through an MX4 layer and an MX4 Monarch map: a token's result does not
+    depend on the batch it came in beyond the two kernels' rounding."""
+    rng = np.random.default_rng(12)
+    shape = dict(nb1=16, in1=32, out1=32, nb2=16, in2=32, out2=32, out_transpose=0)
+    W, _ = dev(rng.uniform(-1, 1, (1, 512, 512)) / 22, "bf16")
+    R, _ = dev(rng.uniform(-1, 1, (16, 32, 32)) / 5, "bf16")
+    Wq, Rq = bdl.mx4_quantise(W), bdl.mx4_quantise(R)
+    X, _ = dev(rng.standard_normal((300, 512)), "bf16")
+    H = bdl.mx4_linear_fwd(X, Wq)
+    Y = bdl.mx4_fwd(H, Rq, Rq, shape)
+    for r in (0, 1, 150, 299):
+        h = bdl.mx4_linear_fwd(X[r:r + 1], Wq)
+        assert float((h - H[r:r + 1]).abs().max()) <= 2.0 ** -7 * float(H[r].abs().max())
+        y = bdl.mx4_fwd(H[r:r + 1].contiguous(), Rq, Rq, shape)
+        assert float((y - Y[r:r + 1]).float().norm()) <= 2.0 ** -6 * float(Y[r].float().norm())
+
+
+def guarded(shape, dtype):
+    """A tensor inside a larger buffer filled with a pattern, and a check that the rest is untouched."""
+    n = int(np.prod(shape))
+    pad = 256
+    buf = torch.full((n + 2 * pad,), 7.0, dtype=dtype, device="cuda")
+    view = buf[pad:pad + n].view(shape)
+
+    def intact():
+        return bool((buf[:pad] == 7).all() and (buf[pad + n:] == 7).all())
+    return view, intact
+
+
+@pytest.mark.parametrize("rows,nb,inn,out", [(1, 1, 33, 130), (9, 3, 40, 24), (130, 2, 96, 200), (257, 1, 256, 72), (65, 2, 64, 64)])
+def test_nothing_is_written_outside_the_outputs(rows, nb, inn, out):
+    t, _ = layer(rows, nb, inn, out, True, "bf16", seed=4)
+    Wq, Xq = bdl.mx4_quantise(t["W"]), bdl.mx4_quantise(t["X"], nblocks=nb)
+    for X in (t["X"], Xq):
+        Y, ok = guarded((rows, nb * out), torch.bfloat16)
+        want = bdl.mx4_linear_fwd(X, Wq, bias=t["b"])
+        assert torch.equal(bdl.mx4_linear_fwd(X, Wq, bias=t["b"], Y=Y), want) and ok()
+    dX, ok1 = guarded((rows, nb * inn), torch.bfloat16)
+    dW, ok2 = guarded((nb, out, inn), torch.bfloat16)
+    db, ok3 = guarded((nb * out,), torch.bfloat16)
+    want = bdl.mx4_linear_bwd(t["dY"], Xq, Wq, bias=True)
+    need = bdl.mx4_linear_workspace_bytes(rows, nb, inn, out, "bf16", True)
+    ws = torch.full((need + 512,), 9, dtype=torch.uint8, device="cuda")
+    got = bdl.mx4_linear_bwd(t["dY"], Xq, Wq, bias=True, dX=dX, dW=dW, dbias=db, workspace=ws[:need])
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and ok1() and ok2() and ok3()
+    assert bool((ws[need:] == 9).all())
+    out_v, ok = guarded((rows, nb * inn), torch.bfloat16)
+    bdl.mx4_dequantise(Xq, "bf16", out=out_v)
+    assert ok()
+
+
+def test_no_rows():
+    W, _ = dev(np.ones((2, 40, 64)), "bf16")
+    Wq = bdl.mx4_quantise(W)
+    X = torch.empty(0, 128, dtype=torch.bfloat16, device="cuda")
+    Xq = bdl.mx4_quantise(X, nblocks=2)
+    assert bdl.mx4_dequantise(Xq).shape == (0, 128)
+    assert bdl.mx4_linear_fwd(X, Wq).shape == (0, 80) and bdl.mx4_linear_fwd(Xq, Wq).shape == (0, 80)
+    dX, dW, db = bdl.mx4_linear_bwd(torch.empty(0, 80, dtype=torch.bfloat16, device="cuda"), Xq, Wq, bias=True)
+    assert dX.shape == (0, 128) and not dW.any() and not db.any()
+    shape = dict(nb1=2, in1=64, out1=40, nb2=2, in2=40, out2=8, out_transpose=1)
+    assert bdl.mx4_fwd(X, Wq, bdl.mx4_quantise(torch.ones(2, 8, 40, dtype=torch.bfloat16, device="cuda")), shape).shape == (0, 16)
+
+
+def everything(t, Wq, Rq, shape, nb, stream=None):
+    Xq = bdl.mx4_quantise(t["X"], nblocks=nb, stream=stream)
+    out = [bdl.mx4_dequantise(Xq, stream=stream), bdl.mx4_linear_fwd(Xq, Wq, bias=t["b"], stream=stream),
+           bdl.mx4_linear_fwd(t["X"], Wq, bias=t["b"], stream=stream), bdl.mx4_fwd(t["X"], Rq, Rq, shape, stream=stream)]
+    return out + list(bdl.mx4_linear_bwd(t["dY"], Xq, Wq, bias=True, stream=stream))
+
+
+@pytest.mark.parametrize("rows", [2, 40, 260])
+def test_captured_graphs_and_streams(rows):
+    """Two graphs of the whole set replayed on two streams at once, new inputs in place, and a call given
+    a stream: all as the plain calls on those inputs."""
+    nb, inn, out = 4, 64, 96
+    shape = dict(nb1=4, in1=64, out1=64, nb2=4, in2=64, out2=64, out_transpose=0)
+    sets, graphs, outs = [], [], []
+    for k in range(2):
+        t, _ = layer(rows, nb, inn, out, True, "bf16", seed=20 + k)
+        R, _ = dev(np.random.default_rng(k).uniform(-1, 1, (4, 64, 64)), "bf16")
+        sets.append((t, bdl.mx4_quantise(t["W"]), bdl.mx4_quantise(R), shape, nb))
+    everything(*sets[0])
+    torch.cuda.synchronize()
+    for s in sets:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(everything(*s))
+        graphs.append(g)
+    new = [layer(rows, nb, inn, out, True, "bf16", seed=30 + k)[0] for k in range(2)]
+    for s, n in zip(sets, new):
+        for k in ("X", "dY", "b"):
+            s[0][k].copy_(n[k])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for s, o in zip(sets, outs):
+        plain = everything(*s)
+        assert all(torch.equal(a, b) for a, b in zip(o, plain))
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        given = everything(*s, stream=side)
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(given, plain))
+    assert bdl.last_device_status() == 0
+
+
+def test_large_offsets():
+    """A tensor whose codes pass 2^31 elements: the last rows are rounded and read where they belong."""
+    rows, cols = 1 << 19, 4100
+    X = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    rng = np.random.default_rng(2)
+    tail, v = dev(rng.standard_normal((3, cols)), "bf16")
+    X[-3:] = tail
+    q = bdl.mx4_quantise(X)
+    del X
+    W, wv = dev(rng.uniform(-1, 1, (1, 8, cols)) / 64, "bf16")
+    Y = bdl.mx4_linear_fwd(q, bdl.mx4_quantise(W))
+    assert not Y[:-3].any()
+    ref = oracle.mx4_linear_forward(oracle.mx4_round(v), oracle.mx4_round(wv))
+    mags = oracle.mx4_linear_forward(np.abs(oracle.mx4_round(v)), np.abs(oracle.mx4_round(wv)))
+    close(Y[-3:], ref, mags, cols + 2, "bf16", "Y")
+    back = bdl.mx4_dequantise(q)
+    assert np.array_equal(f64(back[-3:]), oracle.mx4_round(v)) and not back[:16].any()
