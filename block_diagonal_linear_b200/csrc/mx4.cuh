@@ -119,6 +119,9 @@ struct Mx4Linear {
   Mx4Shape x() const { return Mx4Shape{rows, nb, in}; }
   Mx4Shape w() const { return Mx4Shape{out, nb, in}; }
 };
+// Both operands in MX4 on the block-scaled tensor cores, every size and both types (mx4_tc.cu).
+cudaError_t mx4_tc_fwd(const Mx4View& x, const Mx4View& w, const void* bias, const Mx4Linear& d, void* Y, int* status,
+                       cudaStream_t st);
 // Tiled FMA kernels for every size and type (mx4_generic.cu).
 cudaError_t mx4_generic_fwd(const Mx4View& x, const Mx4View& w, const void* bias, const Mx4Linear& d, void* Y,
                             cudaStream_t st);
