@@ -84,6 +84,8 @@ int check_monarch(const monarch_dims* d) {
   return check_size(d->out2, d->nb2, d->in2, d->dtype);
 }
 
+// Up to this many rows a plain X goes through the few-rows kernel.
+constexpr int64_t kFewRows = 64;
 // Up to this many rows the Monarch map is two products with the middle vector in fp32 in the
 // workspace; longer batches expand the factors there and run the plain forward.
 constexpr int64_t kMonarchFewRows = 64;
@@ -176,8 +178,10 @@ int monarch_mx4_linear_wfwd(const void* X, const void* w_codes, const void* w_sc
                          Range(w_scales, ws.scale_bytes()), Range(d.has_bias ? bias : nullptr, n_out * es)})) != MONARCH_OK)
     return rc;
   const Mx4View w{(const uint8_t*)w_codes, (const uint8_t*)w_scales, ws};
-  return status_of(mx4_generic_wfwd(X, d.dtype, w, d.has_bias ? bias : nullptr, d.rows, Mx4Out::blocks(d.nb, d.out), Y,
-                                    d.dtype, (cudaStream_t)stream));
+  const Mx4Out o = Mx4Out::blocks(d.nb, d.out);
+  const void* b = d.has_bias ? bias : nullptr;
+  return status_of(d.rows <= kFewRows ? mx4_rows_fwd(X, d.dtype, w, b, d.rows, o, Y, d.dtype, false, (cudaStream_t)stream)
+                                      : mx4_generic_wfwd(X, d.dtype, w, b, d.rows, o, Y, d.dtype, (cudaStream_t)stream));
 }
 
 int monarch_mx4_linear_bwd(const void* dY, const void* x_codes, const void* x_scales, const void* w_codes,
@@ -233,12 +237,14 @@ int monarch_mx4_fwd(const void* X, const void* r_codes, const void* r_scales, co
   const Mx4View r{(const uint8_t*)r_codes, (const uint8_t*)r_scales, rs}, l{(const uint8_t*)l_codes, (const uint8_t*)l_scales, ls};
   cudaStream_t st = (cudaStream_t)stream;
   if (s.rows <= kMonarchFewRows) {
-    // U = blockdiag(R) X, written through P, then blockdiag(L) of contiguous slices, through P_out
-    cudaError_t e = mx4_generic_wfwd(X, d->dtype, r, nullptr, s.rows, Mx4Out::transposed(s.nb1, s.out1), workspace, MONARCH_F32, st);
-    if (e != cudaSuccess) return MONARCH_ERR_CUDA;
-    return status_of(mx4_generic_wfwd(workspace, MONARCH_F32, l, nullptr, s.rows,
-                                      s.out_transpose ? Mx4Out::transposed(s.nb2, s.out2) : Mx4Out::blocks(s.nb2, s.out2), Y,
-                                      d->dtype, st));
+    // U = blockdiag(R) X, written through P, then blockdiag(L) of contiguous slices, through P_out.  The
+    // second kernel may ask for L at once: whatever wrote it had ended when the first began.
+    if (mx4_rows_fwd(X, d->dtype, r, nullptr, s.rows, Mx4Out::transposed(s.nb1, s.out1), workspace, MONARCH_F32, false, st) !=
+        cudaSuccess)
+      return MONARCH_ERR_CUDA;
+    return status_of(mx4_rows_fwd(workspace, MONARCH_F32, l, nullptr, s.rows,
+                                  s.out_transpose ? Mx4Out::transposed(s.nb2, s.out2) : Mx4Out::blocks(s.nb2, s.out2), Y,
+                                  d->dtype, true, st));
   }
   char* R = (char*)workspace;
   char* L = R + al256((size_t)(s.n_R() * es));

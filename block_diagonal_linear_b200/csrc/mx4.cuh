@@ -80,17 +80,14 @@ __device__ __forceinline__ float decode(uint32_t code) {
   const float a = m < 2 ? 0.5f * (float)m : __uint_as_float(((126u + (m >> 1)) << 23) | ((m & 1u) << 22));
   return (code & 8u) ? -a : a;
 }
-// Eight codes to bf16 pairs without their scale, divided by 2^126: the E2M1 exponent and mantissa
-// bits land on the bf16 ones, so that one multiplication by a power of two finishes the job (a code
-// of 0.5 is a bf16 subnormal here and becomes a normal number by it).  p[i] holds codes 2i, 2i + 1.
+// Eight codes to bf16 without their scale, divided by 2^126: the E2M1 exponent and mantissa bits land
+// on the bf16 ones, so that one multiplication by a power of two finishes the job (a code of 0.5 is a
+// bf16 subnormal here and becomes a normal number by it).  p[j] holds codes j (low half) and j + 4.
 __device__ __forceinline__ void spread8(uint32_t w, uint32_t (&p)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    // codes 2i and 2i+1 sit in bits 8i .. 8i+3 and 8i+4 .. 8i+7
-    const uint32_t c = w >> (8 * i);
-    const uint32_t lo = c & 15u, hi = (c >> 4) & 15u;
-    p[i] = ((lo & 8u) << 12) | ((lo & 7u) << 6) | ((hi & 8u) << 28) | ((hi & 7u) << 22);
-  }
+  p[0] = ((w << 12) & 0x80008000u) | ((w << 6) & 0x01c001c0u);
+  p[1] = ((w << 8) & 0x80008000u) | ((w << 2) & 0x01c001c0u);
+  p[2] = ((w << 4) & 0x80008000u) | ((w >> 2) & 0x01c001c0u);
+  p[3] = (w & 0x80008000u) | ((w >> 6) & 0x01c001c0u);
 }
 
 }  // namespace mx4
@@ -122,9 +119,11 @@ struct Mx4Linear {
 // Both operands in MX4 on the block-scaled tensor cores, every size and both types (mx4_tc.cu).
 cudaError_t mx4_tc_fwd(const Mx4View& x, const Mx4View& w, const void* bias, const Mx4Linear& d, void* Y, int* status,
                        cudaStream_t st);
+// X as it is, few rows (mx4_rows.cu); X, Y fp32 or bf16.  w_early: no kernel of the stream that may still
+// run writes the weight, so it may be read ahead of the grid-dependency wait.
+cudaError_t mx4_rows_fwd(const void* X, int x_dtype, const Mx4View& w, const void* bias, int64_t rows, const Mx4Out& o, void* Y,
+                         int y_dtype, bool w_early, cudaStream_t st);
 // Tiled FMA kernels for every size and type (mx4_generic.cu).
-cudaError_t mx4_generic_fwd(const Mx4View& x, const Mx4View& w, const void* bias, const Mx4Linear& d, void* Y,
-                            cudaStream_t st);
 // X (rows, nb * in) as it is; X and Y may differ in type (bias has Y's).
 cudaError_t mx4_generic_wfwd(const void* X, int x_dtype, const Mx4View& w, const void* bias, int64_t rows, const Mx4Out& o,
                              void* Y, int y_dtype, cudaStream_t st);

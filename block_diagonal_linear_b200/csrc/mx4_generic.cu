@@ -166,14 +166,6 @@ cudaError_t dbias_t(const void* dY, int64_t rows, int64_t cols, float* part, voi
 
 }  // namespace
 
-cudaError_t mx4_generic_fwd(const Mx4View& x, const Mx4View& w, const void* bias, const Mx4Linear& d, void* Y,
-                            cudaStream_t st) {
-  const Mx4Out o = Mx4Out::blocks(d.nb, d.out);
-  return d.dtype == MONARCH_BF16
-             ? launch_fma<Mx4Rows, Mx4Rows, __nv_bfloat16>({x}, {w}, d.rows, d.out, d.in, d.nb, o, bias, Y, st)
-             : launch_fma<Mx4Rows, Mx4Rows, float>({x}, {w}, d.rows, d.out, d.in, d.nb, o, bias, Y, st);
-}
-
 template <typename TX, typename TY>
 static cudaError_t generic_wfwd_t(const void* X, const Mx4View& w, const void* bias, int64_t rows, const Mx4Out& o, void* Y,
                                   cudaStream_t st) {
