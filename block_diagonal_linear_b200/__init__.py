@@ -51,8 +51,8 @@ EXPORTED = (
     "monarch_dyad_path", "monarch_dyad_fwd", "monarch_dyad_bwd", "monarch_lattice_workspace_bytes",
     "monarch_lattice_path", "monarch_lattice_weight_elems", "monarch_lattice_fwd", "monarch_lattice_bwd",
     "monarch_mx4_code_bytes", "monarch_mx4_scale_bytes", "monarch_mx4_quantise", "monarch_mx4_dequantise",
-    "monarch_mx4_linear_workspace_bytes", "monarch_mx4_linear_fwd", "monarch_mx4_linear_wfwd",
-    "monarch_mx4_linear_bwd", "monarch_mx4_fwd_workspace_bytes", "monarch_mx4_fwd",
+    "monarch_mx4_linear_wfwd_workspace_bytes", "monarch_mx4_linear_bwd_workspace_bytes",
+    "monarch_mx4_linear_fwd", "monarch_mx4_linear_wfwd", "monarch_mx4_linear_bwd", "monarch_mx4_fwd_workspace_bytes", "monarch_mx4_fwd",
 )
 
 
@@ -210,7 +210,7 @@ def lib() -> ctypes.CDLL:
                 ("monarch_mx4_code_bytes", [qp], sz), ("monarch_mx4_scale_bytes", [qp], sz),
                 ("monarch_mx4_quantise", [vp, qp, vp, vp, vp], ctypes.c_int),
                 ("monarch_mx4_dequantise", [vp, vp, qp, vp, vp], ctypes.c_int),
-                ("monarch_mx4_linear_workspace_bytes", [mp], sz),
+                ("monarch_mx4_linear_wfwd_workspace_bytes", [mp], sz), ("monarch_mx4_linear_bwd_workspace_bytes", [mp], sz),
                 ("monarch_mx4_linear_fwd", [vp, vp, vp, vp, vp, mp, vp, vp], ctypes.c_int),
                 ("monarch_mx4_linear_wfwd", [vp, vp, vp, vp, mp, vp, vp, sz, vp], ctypes.c_int),
                 ("monarch_mx4_linear_bwd", [vp, vp, vp, vp, vp, mp, vp, vp, vp, vp, sz, vp], ctypes.c_int),

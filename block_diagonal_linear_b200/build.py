@@ -14,7 +14,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libmonarch.so")
 SOURCES = ["api.cu", "generic.cu", "tc_fwd.cu", "tc_rows.cu", "tc_wide.cu", "tc_split.cu", "tc_stage.cu", "tc_gemm.cu", "tc_pair.cu",
            "bwd_fast.cu", "bwd_gemm.cu", "linear.cu", "project.cu", "dyad.cu", "lattice.cu", "noalloc.cu",
-           "mx4.cu", "mx4_quant.cu", "mx4_generic.cu", "mx4_tc.cu", "mx4_rows.cu"]
+           "mx4.cu", "mx4_quant.cu", "mx4_gemm.cu", "mx4_tc.cu", "mx4_rows.cu"]
 HEADERS = ["common.cuh", "ptx.cuh", "tc_common.cuh", "tc_gemm.cuh", "mx4.cuh"]
 
 NVCC_FLAGS = [

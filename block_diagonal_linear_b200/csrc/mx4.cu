@@ -70,8 +70,14 @@ int check_workspace(const void* ws, size_t have, size_t need) {
 
 int status_of(cudaError_t e) { return e == cudaSuccess ? MONARCH_OK : MONARCH_ERR_CUDA; }
 
-size_t linear_workspace(const Mx4Linear& d) {
-  return d.has_bias ? al256(mx4_dbias_bytes(d.rows, (int64_t)d.nb * d.out)) : 0;
+// Up to this many rows a plain X goes through the few-rows kernel.
+constexpr int64_t kFewRows = 64;
+
+size_t wfwd_workspace(const Mx4Linear& d) { return d.rows <= kFewRows ? 0 : mx4_gemm_fwd_bytes(d); }
+// Backward: the two products' scratch, then the bias gradient's.
+size_t bwd_workspace(const Mx4Linear& d) {
+  if (d.rows == 0) return 0;
+  return mx4_gemm_bwd_bytes(d) + (d.has_bias ? al256(mx4_dbias_bytes(d.rows, (int64_t)d.nb * d.out)) : 0);
 }
 
 Mx4Shape r_shape(const monarch_dims& d) { return Mx4Shape{d.out1, d.nb1, d.in1}; }
@@ -84,8 +90,6 @@ int check_monarch(const monarch_dims* d) {
   return check_size(d->out2, d->nb2, d->in2, d->dtype);
 }
 
-// Up to this many rows a plain X goes through the few-rows kernel.
-constexpr int64_t kFewRows = 64;
 // Up to this many rows the Monarch map is two products with the middle vector in fp32 in the
 // workspace; longer batches expand the factors there and run the plain forward.
 constexpr int64_t kMonarchFewRows = 64;
@@ -136,8 +140,11 @@ int monarch_mx4_dequantise(const void* codes, const void* scales, const monarch_
   return status_of(mx4_dequantise(q, d->by_block != 0, d->dtype, X, (cudaStream_t)stream));
 }
 
-size_t monarch_mx4_linear_workspace_bytes(const monarch_mx4_linear_dims* d) {
-  return check(d) != MONARCH_OK ? 0 : linear_workspace(to_linear(*d));
+size_t monarch_mx4_linear_wfwd_workspace_bytes(const monarch_mx4_linear_dims* d) {
+  return check(d) != MONARCH_OK ? 0 : wfwd_workspace(to_linear(*d));
+}
+size_t monarch_mx4_linear_bwd_workspace_bytes(const monarch_mx4_linear_dims* d) {
+  return check(d) != MONARCH_OK ? 0 : bwd_workspace(to_linear(*d));
 }
 
 int monarch_mx4_linear_fwd(const void* x_codes, const void* x_scales, const void* w_codes, const void* w_scales,
@@ -169,7 +176,7 @@ int monarch_mx4_linear_wfwd(const void* X, const void* w_codes, const void* w_sc
   const Mx4Linear d = to_linear(*ld);
   if ((rc = check_ptrs({X, w_codes, w_scales, Y})) != MONARCH_OK) return rc;
   if (d.has_bias && (rc = check_ptrs({bias})) != MONARCH_OK) return rc;
-  const size_t need = linear_workspace(d);
+  const size_t need = wfwd_workspace(d);
   if ((rc = check_workspace(workspace, workspace_bytes, need)) != MONARCH_OK) return rc;
   const int64_t es = elem_bytes(d.dtype), n_out = (int64_t)d.nb * d.out;
   const Mx4Shape ws = d.w();
@@ -178,10 +185,13 @@ int monarch_mx4_linear_wfwd(const void* X, const void* w_codes, const void* w_sc
                          Range(w_scales, ws.scale_bytes()), Range(d.has_bias ? bias : nullptr, n_out * es)})) != MONARCH_OK)
     return rc;
   const Mx4View w{(const uint8_t*)w_codes, (const uint8_t*)w_scales, ws};
-  const Mx4Out o = Mx4Out::blocks(d.nb, d.out);
   const void* b = d.has_bias ? bias : nullptr;
-  return status_of(d.rows <= kFewRows ? mx4_rows_fwd(X, d.dtype, w, b, d.rows, o, Y, d.dtype, false, (cudaStream_t)stream)
-                                      : mx4_generic_wfwd(X, d.dtype, w, b, d.rows, o, Y, d.dtype, (cudaStream_t)stream));
+  cudaStream_t st = (cudaStream_t)stream;
+  if (d.rows <= kFewRows)
+    return status_of(mx4_rows_fwd(X, d.dtype, w, b, d.rows, Mx4Out::blocks(d.nb, d.out), Y, d.dtype, false, st));
+  int* status = status_ptr();
+  if (status == nullptr) return MONARCH_ERR_CUDA;
+  return status_of(mx4_gemm_fwd(X, w, b, d, Y, workspace, status, st));
 }
 
 int monarch_mx4_linear_bwd(const void* dY, const void* x_codes, const void* x_scales, const void* w_codes,
@@ -196,7 +206,7 @@ int monarch_mx4_linear_bwd(const void* dY, const void* x_codes, const void* x_sc
   if (d.rows > 0 && dW != nullptr && (rc = check_ptrs({x_codes, x_scales, dW})) != MONARCH_OK) return rc;
   if (dW != nullptr && !aligned16(dW)) return MONARCH_ERR_ALIGN;
   if (d.has_bias && (rc = check_ptrs({dbias})) != MONARCH_OK) return rc;
-  const size_t need = linear_workspace(d);
+  const size_t need = bwd_workspace(d);
   if ((rc = check_workspace(workspace, workspace_bytes, need)) != MONARCH_OK) return rc;
   const int64_t es = elem_bytes(d.dtype), n_out = (int64_t)d.nb * d.out;
   const Mx4Shape xs = d.x(), ws = d.w();
@@ -207,12 +217,16 @@ int monarch_mx4_linear_bwd(const void* dY, const void* x_codes, const void* x_sc
     return rc;
   const Mx4View x{(const uint8_t*)x_codes, (const uint8_t*)x_scales, xs}, w{(const uint8_t*)w_codes, (const uint8_t*)w_scales, ws};
   cudaStream_t st = (cudaStream_t)stream;
-  if (d.rows > 0 && dX != nullptr && mx4_generic_bwd_x(dY, w, d, dX, st) != cudaSuccess) return MONARCH_ERR_CUDA;
-  if (dW != nullptr) {  // no rows: zero
-    const cudaError_t e = d.rows > 0 ? mx4_generic_bwd_w(dY, x, d, dW, st) : cudaMemsetAsync(dW, 0, (size_t)(n_out * d.in * es), st);
-    if (e != cudaSuccess) return MONARCH_ERR_CUDA;
+  if (d.rows == 0) {  // nothing to sum
+    if (dW != nullptr && cudaMemsetAsync(dW, 0, (size_t)(n_out * d.in * es), st) != cudaSuccess) return MONARCH_ERR_CUDA;
+    return d.has_bias ? status_of(cudaMemsetAsync(dbias, 0, (size_t)(n_out * es), st)) : MONARCH_OK;
   }
-  return d.has_bias ? status_of(mx4_dbias(dY, d.rows, n_out, d.dtype, (float*)workspace, dbias, st)) : MONARCH_OK;
+  int* status = status_ptr();
+  if (status == nullptr) return MONARCH_ERR_CUDA;
+  if ((dX != nullptr || dW != nullptr) && mx4_gemm_bwd(dY, x, w, d, dX, dW, workspace, status, st) != cudaSuccess)
+    return MONARCH_ERR_CUDA;
+  float* part = (float*)((char*)workspace + mx4_gemm_bwd_bytes(d));
+  return d.has_bias ? status_of(mx4_dbias(dY, d.rows, n_out, d.dtype, part, dbias, st)) : MONARCH_OK;
 }
 
 size_t monarch_mx4_fwd_workspace_bytes(const monarch_dims* d) {

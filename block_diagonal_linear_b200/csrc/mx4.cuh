@@ -123,12 +123,14 @@ cudaError_t mx4_tc_fwd(const Mx4View& x, const Mx4View& w, const void* bias, con
 // run writes the weight, so it may be read ahead of the grid-dependency wait.
 cudaError_t mx4_rows_fwd(const void* X, int x_dtype, const Mx4View& w, const void* bias, int64_t rows, const Mx4Out& o, void* Y,
                          int y_dtype, bool w_early, cudaStream_t st);
-// Tiled FMA kernels for every size and type (mx4_generic.cu).
-// X (rows, nb * in) as it is; X and Y may differ in type (bias has Y's).
-cudaError_t mx4_generic_wfwd(const void* X, int x_dtype, const Mx4View& w, const void* bias, int64_t rows, const Mx4Out& o,
-                             void* Y, int y_dtype, cudaStream_t st);
-cudaError_t mx4_generic_bwd_x(const void* dY, const Mx4View& w, const Mx4Linear& d, void* dX, cudaStream_t st);
-cudaError_t mx4_generic_bwd_w(const void* dY, const Mx4View& x, const Mx4Linear& d, void* dW, cudaStream_t st);
+// Products with a plain operand on the bf16 tensor cores, every size and both types (mx4_gemm.cu); ws: the
+// bytes that the size query gives.  dX or dW may be NULL.
+size_t mx4_gemm_fwd_bytes(const Mx4Linear& d);
+cudaError_t mx4_gemm_fwd(const void* X, const Mx4View& w, const void* bias, const Mx4Linear& d, void* Y, void* ws, int* status,
+                         cudaStream_t st);
+size_t mx4_gemm_bwd_bytes(const Mx4Linear& d);
+cudaError_t mx4_gemm_bwd(const void* dY, const Mx4View& x, const Mx4View& w, const Mx4Linear& d, void* dX, void* dW, void* ws,
+                         int* status, cudaStream_t st);
 // dbias[c] = sum over rows of dY[r][c], rows in a fixed order; part: mx4_dbias_bytes of scratch.
 size_t mx4_dbias_bytes(int64_t rows, int64_t cols);
 cudaError_t mx4_dbias(const void* dY, int64_t rows, int64_t cols, int dtype, float* part, void* dbias,

@@ -1,0 +1,714 @@
+// Products of a plain tensor with MX4 values on the bf16 tensor cores (tcgen05 kind::f16):
+//
+//   forward   Y[r][b*out + o]  = sum_i X[r][b*in + i] W^[b][o][i] (+ bias)     A = X,  B = W^
+//   backward  dX[r][b*in + i]  = sum_o dY[r][b*out + o] W^[b][o][i]            A = dY, B = W^ (inner index N)
+//             dW[b][o][i]      = sum_r dY[r][b*out + o] X^[b][r][i]            A = dY, B = X^ (rows as K)
+//
+// MX4 values are exact in bf16, so the MX4 operand is expanded once into the workspace (2 bytes a
+// value against the product's 2 * rows operations on it) and the product is a bf16 GEMM with fp32
+// sums.  A plain bf16 operand whose rows TMA can address (16-byte multiples) is read where it is;
+// others are copied into padded rows first, and fp32 ones are cut into three bf16 parts there, which
+// hold all 24 bits: the product then runs over K three times, once a part, smallest part first,
+// against the same B.
+//
+// One kernel: D = A B^T per block in 256 x 256 tiles on CTA pairs (cta_group::2: each CTA loads half of
+// A and half of B, so a stage of K = 64 costs an SM 32 KB for a 128 x 256 share), or in 128 x 128
+// tiles on single CTAs where there are too few large tiles.  Either operand may have K as its inner
+// index (rows of 128 swizzled bytes) or its M / N index (chunks of 64 x 64); all tensor maps are per
+// block, so tiles that hang over a block's edge read zeros and write nothing there.  A long K with few
+// tiles is split; the parts are written in fp32 and summed in order.
+// Roles: warp 0 TMA producer, warp 1 MMA issuer (of the pair's first CTA), warps 2..5 epilogue.
+#include <algorithm>
+
+#include "mx4.cuh"
+#include "tc_common.cuh"
+
+namespace monarch {
+
+namespace {
+
+constexpr int kThreads = 192;
+constexpr int kEpiWarps = 4;
+constexpr int kStagingChunk = 128 * 128;
+
+struct GJob {
+  int nb, mtiles, ntiles, nsplit;
+  int64_t units;
+  int64_t m;           // rows of D, for the epilogue without TMA
+  int n;               // columns of D per block
+  int64_t d_b, d_m;    // D strides (elements) of a block and a row, for the epilogue without TMA
+  int nk, parts;       // K stages of one part; parts of A
+  int stages_per_split;
+  int a_chunked, b_chunked;  // inner index M / N: the map is 4-D and both 64-wide chunks are one box
+};
+
+template <bool PAIR_, bool A_MN_, bool B_MN_, typename T_, bool TMA_OUT_>
+struct GCfg {
+  static constexpr bool PAIR = PAIR_, A_MN = A_MN_, B_MN = B_MN_, TMA_OUT = TMA_OUT_;
+  using T = T_;
+  static constexpr int BN = PAIR ? 256 : 128;
+  static constexpr int BM = PAIR ? 256 : 128;              // rows of a unit; 128 per CTA
+  static constexpr int A_BYTES = 128 * 128, B_BYTES = 128 * 128;  // this CTA's 128 rows of each, K = 64
+  static constexpr int STAGE = A_BYTES + B_BYTES;
+  static constexpr int NSTAGE = 5;
+  static constexpr int SMEM_BYTES = 2 * kStagingChunk + NSTAGE * STAGE + 2048 + 1024;
+  static constexpr int TMEM_COLS = 2 * BN;
+  static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
+};
+
+struct GBars {
+  uint64_t full[8], empty[8];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t mma_done;
+  uint32_t tmem_base;
+  int abort_flag;
+  float bias[256];
+};
+static_assert(sizeof(GBars) <= 2048, "bars");
+
+struct GUnit {
+  int b, mt, nt, split;
+};
+// n tile fastest, then block, m tile, split
+__device__ __forceinline__ GUnit unit_at(const GJob& j, int64_t u) {
+  GUnit c;
+  c.nt = (int)(u % j.ntiles);
+  u /= j.ntiles;
+  c.b = (int)(u % j.nb);
+  u /= j.nb;
+  c.mt = (int)(u % j.mtiles);
+  c.split = (int)(u / j.mtiles);
+  return c;
+}
+__device__ __forceinline__ void stage_range(const GJob& j, int split, int* lo, int* hi) {
+  *lo = split * j.stages_per_split;
+  *hi = min(j.nk * j.parts, *lo + j.stages_per_split);
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void load3(void* dst, const CUtensorMap* m, uint64_t* bar, uint32_t bar0, int x, int y, int z,
+                                      uint64_t pol) {
+  if (PAIR)
+    ptx::tma_load_3d_pair(dst, m, bar0, x, y, z, pol);
+  else
+    ptx::tma_load_3d(dst, m, bar, x, y, z, pol);
+}
+// 128 rows (M or N index r0 ..) x 64 of K (index k0 ..) of one operand.  MN: the inner index of the map is
+// the operand's row.  b_k: the batch coordinate, which for an MN operand may also hold the part.
+template <bool PAIR, bool MN>
+__device__ __forceinline__ void load_operand(uint8_t* dst, const CUtensorMap* m, int chunked, uint64_t* bar, uint32_t bar0,
+                                             int r0, int k0, int b_k, uint64_t pol) {
+  if (!MN) {
+    load3<PAIR>(dst, m, bar, bar0, k0, r0, b_k, pol);
+  } else if (chunked) {
+    if (PAIR)
+      ptx::tma_load_4d_pair(dst, m, bar0, 0, k0, r0 / 64, b_k, pol);
+    else
+      ptx::tma_load_4d(dst, m, bar, 0, k0, r0 / 64, b_k, pol);
+  } else {
+    load3<PAIR>(dst, m, bar, bar0, r0, k0, b_k, pol);
+    load3<PAIR>(dst + 8192, m, bar, bar0, r0 + 64, k0, b_k, pol);
+  }
+}
+
+template <class C>
+__global__ void __launch_bounds__(kThreads, 1)
+    mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                    const __grid_constant__ CUtensorMap tmD, const __grid_constant__ GJob job, const typename C::T* bias,
+                    typename C::T* D, int* status) {
+  using T = typename C::T;
+  constexpr bool PAIR = C::PAIR;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t* stg = smem;
+  uint8_t* ring = smem + 2 * kStagingChunk;
+  GBars* bars = (GBars*)(ring + C::NSTAGE * C::STAGE);
+  int* abort_flag = &bars->abort_flag;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank = PAIR ? ptx::cluster_ctarank() : 0u;
+  const bool first = rank == 0;
+  const int64_t cl = PAIR ? blockIdx.x / 2 : blockIdx.x, ncl = PAIR ? gridDim.x / 2 : gridDim.x;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::NSTAGE; ++i) {
+      ptx::mbar_init(&bars->full[i], 1);
+      ptx::mbar_init(&bars->empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&bars->acc_full[i], 1);
+      ptx::mbar_init(&bars->acc_empty[i], (PAIR ? 2 : 1) * kEpiWarps);
+    }
+    ptx::mbar_init(&bars->mma_done, 1);
+    bars->abort_flag = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 1) {
+    if (PAIR) {
+      ptx::tmem_alloc_pair(&bars->tmem_base, C::TMEM_COLS);
+      ptx::tmem_relinquish_pair();
+    } else {
+      ptx::tmem_alloc(&bars->tmem_base, C::TMEM_COLS);
+      ptx::tmem_relinquish();
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (PAIR) ptx::cluster_sync_all();  // both CTAs' barriers exist and TMEM is allocated
+  ptx::tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+
+  if (warp == 0) {
+    // ================================================================ TMA producer (both CTAs of a pair)
+    if (lane == 0) {
+      ptx::tma_prefetch_desc(&tmA);
+      ptx::tma_prefetch_desc(&tmB);
+      if (C::TMA_OUT) ptx::tma_prefetch_desc(&tmD);
+      const uint64_t pol = ptx::policy_evict_normal();
+      const uint32_t full0 = PAIR ? ptx::mapa_shared(ptx::smem_u32(&bars->full[0]), 0) : 0u;
+      uint32_t it = 0;
+      bool ok = true;
+      for (int64_t u = cl; u < job.units && ok; u += ncl) {
+        const GUnit c = unit_at(job, u);
+        int lo, hi;
+        stage_range(job, c.split, &lo, &hi);
+        const int m0 = c.mt * C::BM + (int)rank * 128, n0 = c.nt * C::BN + (int)rank * 128;
+        for (int kb = lo; kb < hi; ++kb, ++it) {
+          const int st = it % C::NSTAGE;
+          if (!wait_or_abort(&bars->empty[st], ((it / C::NSTAGE) & 1) ^ 1, abort_flag, status)) { ok = false; break; }
+          uint8_t* sa = ring + st * C::STAGE;
+          if (first) ptx::mbar_arrive_expect_tx(&bars->full[st], (PAIR ? 2 : 1) * C::STAGE);
+          const uint32_t fb = full0 + (uint32_t)(st * sizeof(uint64_t));
+          const int part = kb / job.nk, k0 = (kb - part * job.nk) * 64;
+          if (C::A_MN)
+            load_operand<PAIR, true>(sa, &tmA, job.a_chunked, &bars->full[st], fb, m0, k0, c.b * job.parts + part, pol);
+          else
+            load_operand<PAIR, false>(sa, &tmA, 0, &bars->full[st], fb, m0, kb * 64, c.b, pol);
+          load_operand<PAIR, C::B_MN>(sa + C::A_BYTES, &tmB, job.b_chunked, &bars->full[st], fb, n0, k0, c.b, pol);
+        }
+      }
+      if (!PAIR) {  // no copy may still be in flight when the CTA leaves (a pair's MMAs wait for theirs)
+        const uint32_t issued = it;
+        for (uint32_t k = (issued > (uint32_t)C::NSTAGE ? issued - C::NSTAGE : 0); k < issued; ++k)
+          ptx::mbar_wait_bounded(&bars->full[k % C::NSTAGE], (k / C::NSTAGE) & 1, kWaitLimitNs);
+      }
+    }
+  } else if (warp == 1) {
+    // ================================================================ MMA issuer (the pair's first CTA)
+    if (first) {
+      constexpr uint32_t idesc = make_idesc(C::BM, C::BN) | (C::A_MN ? 1u << 15 : 0u) | (C::B_MN ? 1u << 16 : 0u);
+      const uint32_t ra = ptx::smem_u32(ring), rb = ra + C::A_BYTES;
+      const uint64_t dA = C::A_MN ? make_sdesc_lbo(ra, 8192, 1024, 2) : make_sdesc(ra, 1024, 2);
+      const uint64_t dB = C::B_MN ? make_sdesc_lbo(rb, 8192, 1024, 2) : make_sdesc(rb, 1024, 2);
+      constexpr uint64_t ka = (C::A_MN ? 2048 : 32) >> 4, kb_ = (C::B_MN ? 2048 : 32) >> 4;
+      uint32_t it = 0, n = 0;
+      bool ok = true;
+      for (int64_t u = cl; u < job.units && ok; u += ncl, ++n) {
+        const GUnit c = unit_at(job, u);
+        int lo, hi;
+        stage_range(job, c.split, &lo, &hi);
+        const int slot = n & 1;
+        if (!warp_wait_or_abort(lane, &bars->acc_empty[slot], ((n >> 1) & 1) ^ 1, abort_flag, status)) { ok = false; break; }
+        ptx::tc_fence_after();
+        const uint32_t d = tmem + slot * C::BN;
+        for (int kb = lo; kb < hi; ++kb, ++it) {
+          const int st = it % C::NSTAGE;
+          if (!warp_wait_or_abort(lane, &bars->full[st], (it / C::NSTAGE) & 1, abort_flag, status)) { ok = false; break; }
+          ptx::tc_fence_after();
+          const uint64_t soff = (uint64_t)((st * C::STAGE) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint32_t acc = (kb > lo || kk > 0) ? 1u : 0u;
+            if (PAIR)
+              ptx::mma_bf16_ss_pair_elect(d, dA + soff + kk * ka, dB + soff + kk * kb_, idesc, acc);
+            else
+              ptx::mma_bf16_ss_elect(d, dA + soff + kk * ka, dB + soff + kk * kb_, idesc, acc);
+          }
+          if (PAIR)
+            ptx::mma_commit_pair_elect(&bars->empty[st], 0x3);
+          else
+            ptx::mma_commit_elect(&bars->empty[st]);
+        }
+        if (!ok) break;
+        if (PAIR)
+          ptx::mma_commit_pair_elect(&bars->acc_full[slot], 0x3);
+        else
+          ptx::mma_commit_elect(&bars->acc_full[slot]);
+      }
+      if (PAIR)
+        ptx::mma_commit_pair_elect(&bars->mma_done, 0x3);
+      else
+        ptx::mma_commit_elect(&bars->mma_done);
+    }
+    if (lane == 0) wait_mma_done(&bars->mma_done, abort_flag, status);
+    __syncwarp();
+  } else {
+    // ================================================================ epilogue (4 warps a CTA)
+    constexpr int CC = 128 / (int)sizeof(T);  // columns of a 128-byte chunk
+    constexpr int NCH = C::BN / CC;
+    const int quad = warp & 3;
+    const int r = quad * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    const int et = threadIdx.x - 64;
+    const bool leader = et == 0;
+    const uint32_t stg_s = ptx::smem_u32(stg);
+    const uint32_t acc_empty0 = PAIR ? ptx::mapa_shared(ptx::smem_u32(&bars->acc_empty[0]), 0) : 0u;
+    uint32_t n = 0, chunk_n = 0;
+    bool ok = true;
+    for (int64_t u = cl; u < job.units && ok; u += ncl, ++n) {
+      const GUnit c = unit_at(job, u);
+      const int slot = n & 1;
+      const int n0 = c.nt * C::BN;
+      const int64_t m0 = (int64_t)c.mt * C::BM + (int64_t)rank * 128;
+      const int blk = c.split * job.nb + c.b;
+      if (bias != nullptr) {
+        ptx::named_bar_sync(1, kEpiWarps * 32);  // the previous tile's bias has been read
+        for (int i = et; i < C::BN; i += kEpiWarps * 32)
+          bars->bias[i] = n0 + i < job.n ? mx4::load(bias + (int64_t)c.b * job.n + n0 + i) : 0.f;
+      }
+      // one verdict for the four warps: none may leave while another waits for it at a barrier
+      ok = ptx::named_bar_all(1, kEpiWarps * 32, wait_or_abort(&bars->acc_full[slot], (n >> 1) & 1, abort_flag, status));
+      if (!ok) break;
+      ptx::tc_fence_after();
+      const uint32_t tb = tmem + lane_off + slot * C::BN;
+      for (int ch = 0; ch < NCH; ++ch) {
+        if (n0 + ch * CC >= job.n || m0 >= job.m) break;  // behind the block's last column or row
+        uint32_t v[CC];
+#pragma unroll
+        for (int q = 0; q < CC / 16; ++q) {
+          uint32_t t16[16];
+          ptx::tmem_ld16(tb + ch * CC + q * 16, t16);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[q * 16 + e] = t16[e];
+        }
+        ptx::tmem_wait_ld();
+        if (bias != nullptr) {
+#pragma unroll
+          for (int e = 0; e < CC; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) + bars->bias[ch * CC + e]);
+        }
+        const int sbuf = chunk_n++ & 1;
+        if (C::TMA_OUT && leader) ptx::bulk_wait_read_allbut1();  // what last left this buffer has been read
+        ptx::named_bar_sync(2, kEpiWarps * 32);
+        const uint32_t base = stg_s + sbuf * kStagingChunk + r * 128;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const uint32_t at = base + (((uint32_t)q ^ (uint32_t)(r & 7)) << 4);
+          if (sizeof(T) == 2)
+            ptx::st_shared_v4(at, ptx::pack_bf16x2(__uint_as_float(v[(8 * q + 0) % CC]), __uint_as_float(v[(8 * q + 1) % CC])),
+                              ptx::pack_bf16x2(__uint_as_float(v[(8 * q + 2) % CC]), __uint_as_float(v[(8 * q + 3) % CC])),
+                              ptx::pack_bf16x2(__uint_as_float(v[(8 * q + 4) % CC]), __uint_as_float(v[(8 * q + 5) % CC])),
+                              ptx::pack_bf16x2(__uint_as_float(v[(8 * q + 6) % CC]), __uint_as_float(v[(8 * q + 7) % CC])));
+          else
+            ptx::st_shared_v4(at, v[(4 * q) % CC], v[(4 * q + 1) % CC], v[(4 * q + 2) % CC], v[(4 * q + 3) % CC]);
+        }
+        if (C::TMA_OUT) {
+          ptx::fence_proxy_async_smem();
+          ptx::named_bar_sync(2, kEpiWarps * 32);
+          if (leader) {
+            ptx::tma_store_3d(&tmD, stg + sbuf * kStagingChunk, n0 + ch * CC, blk, (int)m0);
+            ptx::bulk_commit_group();
+          }
+        } else {
+          // a row pitch that is no multiple of 16 bytes: each warp writes its own 32 rows
+          __syncwarp();
+          const int cols = job.n - n0 - ch * CC;
+          for (int rr = 0; rr < 32; ++rr) {
+            const int64_t row = m0 + quad * 32 + rr;
+            if (row >= job.m) break;
+            const uint8_t* src = stg + sbuf * kStagingChunk + (quad * 32 + rr) * 128;
+            T* dst = D + row * job.d_m + blk * job.d_b + n0 + ch * CC;
+#pragma unroll
+            for (int e = 0; e < CC / 32; ++e) {
+              const int col = e * 32 + lane, byte = col * (int)sizeof(T);
+              if (col < cols) dst[col] = *(const T*)(src + (((byte >> 4) ^ (rr & 7)) << 4) + (byte & 15));
+            }
+          }
+        }
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (first)
+          ptx::mbar_arrive(&bars->acc_empty[slot]);
+        else
+          ptx::mbar_arrive_cluster(acc_empty0 + (uint32_t)(slot * sizeof(uint64_t)));
+      }
+    }
+    if (C::TMA_OUT && leader) ptx::bulk_wait_all();
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (PAIR) ptx::cluster_sync_all();  // neither CTA leaves while the pair's MMAs or its peer may use it
+  ptx::tc_fence_after();
+  if (warp == 1) {
+    if (PAIR)
+      ptx::tmem_dealloc_pair(tmem, C::TMEM_COLS);
+    else
+      ptx::tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// ---------------------------------------------------------------- operand preparation
+// out[b][r][c] = value of element (b, r, c), zero for cols <= c < pitch (a multiple of 8).  One thread
+// turns 8 codes into 16 bytes; bound by the write of 2 bytes a value.
+__global__ void __launch_bounds__(256) mx4_expand_kernel(Mx4View q, __nv_bfloat16* __restrict__ out, int pitch) {
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  const int words = pitch / 8;
+  const int64_t total = (int64_t)q.s.nblocks * q.s.rows * words;
+  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += (int64_t)gridDim.x * 256) {
+    const int64_t row = e / words;
+    const int c = (int)(e - row * words);
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (c * 8 < q.s.kblocks() * 32) {
+      const int b = (int)(row / q.s.rows);
+      const int64_t r = row - (int64_t)b * q.s.rows;
+      const uint32_t w = *(const uint32_t*)(q.codes + row * q.s.pitch() + c * 4);
+      const float f = mx4::scale_value(q.scales[q.s.scale_at(b, r, c >> 2)]);
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = mx4::decode((w >> (4 * i)) & 15u) * f;
+      v = make_uint4(ptx::pack_bf16x2(x[0], x[1]), ptx::pack_bf16x2(x[2], x[3]), ptx::pack_bf16x2(x[4], x[5]),
+                     ptx::pack_bf16x2(x[6], x[7]));
+    }
+    *(uint4*)(out + row * pitch + c * 8) = v;
+  }
+}
+
+// out[r][b][p][c] = part p of X[r][b*cols + c], zero behind cols; PARTS = 1 copies bf16, PARTS = 3 cuts
+// fp32 into three bf16 parts, the smallest first (see above; infinities and NaN stay in the largest).
+template <typename T, int PARTS>
+__global__ void __launch_bounds__(256) mx4_stage_kernel(const T* __restrict__ X, int64_t nrb, int cols,
+                                                        __nv_bfloat16* __restrict__ out, int pitch) {
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  const int words = pitch / 2;
+  const int64_t total = nrb * words;
+  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += (int64_t)gridDim.x * 256) {
+    const int64_t row = e / words;  // (r, b)
+    const int c = (int)(e - row * words) * 2;
+    float x[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) x[i] = c + i < cols ? mx4::load(X + row * cols + c + i) : 0.f;
+    uint32_t* dst = (uint32_t*)(out + row * PARTS * pitch + c);
+#pragma unroll
+    for (int p = PARTS - 1; p >= 0; --p) {
+      dst[p * words] = (__float_as_uint(x[0]) >> 16) | (__float_as_uint(x[1]) & 0xffff0000u);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t top = __float_as_uint(x[i]) & 0xffff0000u;
+        x[i] = (top & 0x7f800000u) == 0x7f800000u ? 0.f : x[i] - __uint_as_float(top);
+      }
+    }
+  }
+}
+
+// out[e] = sum over s of part[s][e], in order.
+template <typename T>
+__global__ void __launch_bounds__(256) mx4_sum_kernel(const float* __restrict__ part, int64_t n, int nsplit, T* __restrict__ out) {
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < n; e += (int64_t)gridDim.x * 256) {
+    float acc = 0.f;
+    for (int s = 0; s < nsplit; ++s) acc += part[(int64_t)s * n + e];
+    st_from_f32(out + e, acc);
+  }
+}
+
+// ---------------------------------------------------------------- bias gradient
+// Column sums of dY in two steps: every CTA sums kBiasRows rows of 64 columns in fp32 (four row
+// lanes, joined in a fixed order), then one thread per column adds the parts in order.
+constexpr int kBiasRows = 256, kBiasCols = 64;
+
+template <typename T>
+__global__ void __launch_bounds__(256) mx4_dbias_part_kernel(const T* __restrict__ dY, int64_t rows, int64_t cols,
+                                                             float* __restrict__ part) {
+  __shared__ float s[4][kBiasCols];
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  const int c = threadIdx.x % kBiasCols, lane = threadIdx.x / kBiasCols;
+  const int64_t col = (int64_t)blockIdx.y * kBiasCols + c;
+  const int64_t r0 = (int64_t)blockIdx.x * kBiasRows, r1 = r0 + kBiasRows < rows ? r0 + kBiasRows : rows;
+  float acc = 0.f;
+  if (col < cols)
+    for (int64_t r = r0 + lane; r < r1; r += 4) acc += mx4::load(dY + r * cols + col);
+  s[lane][c] = acc;
+  __syncthreads();
+  if (lane == 0 && col < cols) part[(int64_t)blockIdx.x * cols + col] = (s[0][c] + s[1][c]) + (s[2][c] + s[3][c]);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) mx4_dbias_sum_kernel(const float* __restrict__ part, int64_t nparts, int64_t cols,
+                                                            T* __restrict__ dbias) {
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (c >= cols) return;
+  float acc = 0.f;
+  for (int64_t k = 0; k < nparts; ++k) acc += part[k * cols + c];
+  st_from_f32(dbias + c, acc);
+}
+
+template <typename T>
+cudaError_t dbias_t(const void* dY, int64_t rows, int64_t cols, float* part, void* dbias, cudaStream_t st) {
+  const int64_t n = (rows + kBiasRows - 1) / kBiasRows;
+  if (n > 0) {
+    const cudaError_t e = launch_kernel(mx4_dbias_part_kernel<T>, dim3((unsigned)n, (unsigned)((cols + kBiasCols - 1) / kBiasCols)),
+                                        dim3(256), 0, st, true, (const T*)dY, rows, cols, part);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_kernel(mx4_dbias_sum_kernel<T>, dim3((unsigned)((cols + 255) / 256)), dim3(256), 0, st, true,
+                       (const float*)part, n, cols, (T*)dbias);
+}
+
+unsigned blocks_for(int64_t threads) {
+  const int64_t n = (threads + 255) / 256, most = (int64_t)num_sms() * 16;
+  return (unsigned)(n < 1 ? 1 : n < most ? n : most);
+}
+
+int up(int v, int to) { return (v + to - 1) / to * to; }
+size_t al256(size_t b) { return (b + 255) & ~size_t(255); }
+
+// ---------------------------------------------------------------- tensor maps
+bool encode(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* base, const cuuint64_t* dims, const cuuint64_t* strides,
+            const cuuint32_t* box) {
+  EncodeTiledFn enc = get_encode();
+  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return enc != nullptr && enc(m, type, rank, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A bf16 operand: (inner, outer, batch) with strides in elements.
+struct Operand {
+  const void* p;
+  int64_t inner, outer, batch;
+  int64_t s_outer, s_batch;
+};
+bool kmajor_map(CUtensorMap* m, const Operand& o) {
+  const cuuint64_t dims[3] = {(cuuint64_t)o.inner, (cuuint64_t)o.outer, (cuuint64_t)o.batch};
+  const cuuint64_t st[2] = {(cuuint64_t)o.s_outer * 2, (cuuint64_t)o.s_batch * 2};
+  const cuuint32_t box[3] = {64, 128, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, o.p, dims, st, box);
+}
+bool mnmajor_map(CUtensorMap* m, const Operand& o, int* chunked) {
+  *chunked = o.inner % 64 == 0;
+  if (*chunked) {
+    const cuuint64_t dims[4] = {64, (cuuint64_t)o.outer, (cuuint64_t)o.inner / 64, (cuuint64_t)o.batch};
+    const cuuint64_t st[3] = {(cuuint64_t)o.s_outer * 2, 128, (cuuint64_t)o.s_batch * 2};
+    const cuuint32_t box[4] = {64, 64, 2, 1};
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, o.p, dims, st, box);
+  }
+  const cuuint64_t dims[3] = {(cuuint64_t)o.inner, (cuuint64_t)o.outer, (cuuint64_t)o.batch};
+  const cuuint64_t st[2] = {(cuuint64_t)o.s_outer * 2, (cuuint64_t)o.s_batch * 2};
+  const cuuint32_t box[3] = {64, 64, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, o.p, dims, st, box);
+}
+
+// D: columns n, rows m, `batch` blocks; strides in elements.
+struct Result {
+  void* p;
+  int64_t m;
+  int n;
+  int64_t batch, d_m, d_b;
+};
+
+struct Plan {
+  bool pair;
+  int nsplit, per_split, stages;
+};
+// 256 x 256 tiles where they fill at least three quarters of the SM pairs (measured: see the table of
+// tiles in the design notes), else 128 x 128; K is split while the tiles leave SMs idle, down to 8
+// stages of 64 a part.
+Plan plan_for(int64_t m, int n, int nb, int nk, bool may_split) {
+  Plan p;
+  const int64_t big = (m + 255) / 256 * ((n + 255) / 256) * nb, pairs = num_sms() / 2;
+  const int64_t want = may_split && nk >= 16 ? std::min<int64_t>(nk / 8, 1 << 10) : 1;
+  p.stages = nk;
+  p.pair = big * want >= pairs * 3 / 4;
+  const int64_t tiles = p.pair ? big : (m + 127) / 128 * ((n + 127) / 128) * nb, slots = p.pair ? pairs : num_sms();
+  int64_t s = may_split ? slots / tiles : 1;
+  s = std::max<int64_t>(1, std::min(s, want));
+  p.per_split = (int)((nk + s - 1) / s);
+  p.nsplit = (nk + p.per_split - 1) / p.per_split;
+  return p;
+}
+
+template <class C>
+cudaError_t launch(const Operand& a, const Operand& b, const Result& d, const void* bias, GJob j, int* status, cudaStream_t st) {
+  using T = typename C::T;
+  CUtensorMap mA, mB, mD;
+  j.a_chunked = j.b_chunked = 0;
+  if (!(C::A_MN ? mnmajor_map(&mA, a, &j.a_chunked) : kmajor_map(&mA, a)) ||
+      !(C::B_MN ? mnmajor_map(&mB, b, &j.b_chunked) : kmajor_map(&mB, b)))
+    return cudaErrorInvalidValue;
+  if (C::TMA_OUT) {
+    const cuuint64_t dims[3] = {(cuuint64_t)d.n, (cuuint64_t)d.batch, (cuuint64_t)d.m};
+    const cuuint64_t strides[2] = {(cuuint64_t)d.d_b * sizeof(T), (cuuint64_t)d.d_m * sizeof(T)};
+    const cuuint32_t box[3] = {(cuuint32_t)(128 / sizeof(T)), 1, 128};
+    if (!encode(&mD, sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, d.p, dims, strides, box))
+      return cudaErrorInvalidValue;
+  } else {
+    mD = mA;  // unused
+  }
+  j.mtiles = (int)((d.m + C::BM - 1) / C::BM);
+  j.ntiles = (d.n + C::BN - 1) / C::BN;
+  j.units = (int64_t)j.nb * j.mtiles * j.ntiles * j.nsplit;
+  cudaError_t e = ensure_smem_attr((const void*)mx4_gemm_kernel<C>, C::SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  const int64_t slots = C::PAIR ? num_sms() / 2 : num_sms();
+  const int64_t n = j.units < slots ? j.units : slots;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(C::PAIR ? 2 * n : n));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::SMEM_BYTES;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {2, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = C::PAIR ? 2 : 1;
+  e = cudaLaunchKernelEx(&cfg, mx4_gemm_kernel<C>, mA, mB, mD, j, (const T*)bias, (T*)d.p, status);
+  if (e == cudaSuccess) launch_counter().fetch_add(1, std::memory_order_relaxed);
+  return e;
+}
+
+template <bool A_MN, bool B_MN, typename T>
+cudaError_t gemm(const Operand& a, const Operand& b, const Result& d, const void* bias, int nb, int64_t k, int parts, const Plan& p,
+                 int* status, cudaStream_t st) {
+  GJob j = {};
+  j.nb = nb;
+  j.nsplit = p.nsplit;
+  j.m = d.m;
+  j.n = d.n;
+  j.d_b = d.d_b;
+  j.d_m = d.d_m;
+  j.nk = (int)((k + 63) / 64);
+  j.parts = parts;
+  j.stages_per_split = p.per_split;
+  const bool tma = d.d_m * sizeof(T) % 16 == 0 && d.d_b * sizeof(T) % 16 == 0;
+  if (p.pair)
+    return tma ? launch<GCfg<true, A_MN, B_MN, T, true>>(a, b, d, bias, j, status, st)
+               : launch<GCfg<true, A_MN, B_MN, T, false>>(a, b, d, bias, j, status, st);
+  return tma ? launch<GCfg<false, A_MN, B_MN, T, true>>(a, b, d, bias, j, status, st)
+             : launch<GCfg<false, A_MN, B_MN, T, false>>(a, b, d, bias, j, status, st);
+}
+
+int parts_of(int dtype) { return dtype == MONARCH_BF16 ? 1 : 3; }
+// A plain (rows, nb * blk) operand is read where it is if it is bf16 and TMA can address its blocks.
+bool direct(int dtype, int blk) { return dtype == MONARCH_BF16 && blk % 8 == 0; }
+size_t staged_bytes(const Mx4Linear& d, int blk) {
+  return direct(d.dtype, blk) ? 0 : al256((size_t)d.rows * d.nb * parts_of(d.dtype) * up(blk, 64) * 2);
+}
+size_t expanded_bytes(const Mx4Shape& s) { return al256((size_t)s.nblocks * s.rows * up(s.cols, 64) * 2); }
+Plan dw_plan(const Mx4Linear& d) {
+  return plan_for(d.out, d.in, d.nb, (int)((d.rows + 63) / 64) * parts_of(d.dtype), true);
+}
+size_t dw_part_bytes(const Mx4Linear& d) {
+  const Plan p = dw_plan(d);
+  return p.nsplit > 1 ? al256((size_t)p.nsplit * d.nb * d.out * d.in * 4) : 0;
+}
+
+cudaError_t expand(const Mx4View& q, void* out, cudaStream_t st) {
+  const int pitch = up(q.s.cols, 64);
+  return launch_kernel(mx4_expand_kernel, dim3(blocks_for((int64_t)q.s.nblocks * q.s.rows * (pitch / 8))), dim3(256), 0, st, true,
+                       q, (__nv_bfloat16*)out, pitch);
+}
+// The K-major view of a plain operand (staged into `ws` if needed).
+cudaError_t stage(const void* X, const Mx4Linear& d, int blk, void* ws, Operand* o, cudaStream_t st) {
+  const int parts = parts_of(d.dtype);
+  if (direct(d.dtype, blk)) {
+    *o = Operand{X, blk, d.rows, d.nb, (int64_t)d.nb * blk, blk};
+    return cudaSuccess;
+  }
+  const int pitch = up(blk, 64);
+  *o = Operand{ws, (int64_t)parts * pitch, d.rows, d.nb, (int64_t)d.nb * parts * pitch, (int64_t)parts * pitch};
+  const int64_t nrb = d.rows * d.nb;
+  const dim3 grid(blocks_for(nrb * (pitch / 2)));
+  return d.dtype == MONARCH_BF16
+             ? launch_kernel(mx4_stage_kernel<__nv_bfloat16, 1>, grid, dim3(256), 0, st, true, (const __nv_bfloat16*)X, nrb, blk,
+                             (__nv_bfloat16*)ws, pitch)
+             : launch_kernel(mx4_stage_kernel<float, 3>, grid, dim3(256), 0, st, true, (const float*)X, nrb, blk,
+                             (__nv_bfloat16*)ws, pitch);
+}
+// The same operand with its rows as K: one batch entry per (block, part).
+Operand rows_as_k(const Operand& o, const Mx4Linear& d, int blk) {
+  if (direct(d.dtype, blk)) return o;
+  const int parts = parts_of(d.dtype), pitch = up(blk, 64);
+  return Operand{o.p, pitch, o.outer, (int64_t)d.nb * parts, o.s_outer, pitch};
+}
+Operand expanded(const void* p, const Mx4Shape& s) {
+  const int pitch = up(s.cols, 64);
+  return Operand{p, pitch, s.rows, s.nblocks, pitch, (int64_t)pitch * s.rows};
+}
+
+}  // namespace
+
+size_t mx4_gemm_fwd_bytes(const Mx4Linear& d) { return expanded_bytes(d.w()) + staged_bytes(d, d.in); }
+
+cudaError_t mx4_gemm_fwd(const void* X, const Mx4View& w, const void* bias, const Mx4Linear& d, void* Y, void* ws, int* status,
+                         cudaStream_t st) {
+  char* wd = (char*)ws;
+  Operand a;
+  cudaError_t e;
+  if ((e = expand(w, wd, st)) != cudaSuccess) return e;
+  if ((e = stage(X, d, d.in, wd + expanded_bytes(d.w()), &a, st)) != cudaSuccess) return e;
+  const Result r{Y, d.rows, d.out, d.nb, (int64_t)d.nb * d.out, d.out};
+  const Plan p = plan_for(d.rows, d.out, d.nb, (d.in + 63) / 64 * parts_of(d.dtype), false);
+  return d.dtype == MONARCH_BF16 ? gemm<false, false, __nv_bfloat16>(a, expanded(wd, d.w()), r, bias, d.nb, d.in, 1, p, status, st)
+                                 : gemm<false, false, float>(a, expanded(wd, d.w()), r, bias, d.nb, d.in, 3, p, status, st);
+}
+
+size_t mx4_gemm_bwd_bytes(const Mx4Linear& d) {
+  // the expanded operand: W for dX, then X for dW in the same place
+  return std::max(expanded_bytes(d.w()), expanded_bytes(d.x())) + staged_bytes(d, d.out) + dw_part_bytes(d);
+}
+
+cudaError_t mx4_gemm_bwd(const void* dY, const Mx4View& x, const Mx4View& w, const Mx4Linear& d, void* dX, void* dW, void* ws,
+                         int* status, cudaStream_t st) {
+  char* ex = (char*)ws;
+  char* sy = ex + std::max(expanded_bytes(d.w()), expanded_bytes(d.x()));
+  float* part = (float*)(sy + staged_bytes(d, d.out));
+  const bool bf = d.dtype == MONARCH_BF16;
+  const int parts = parts_of(d.dtype);
+  Operand a;
+  cudaError_t e;
+  if ((e = stage(dY, d, d.out, sy, &a, st)) != cudaSuccess) return e;
+  if (dX != nullptr) {
+    if ((e = expand(w, ex, st)) != cudaSuccess) return e;
+    const Result r{dX, d.rows, d.in, d.nb, (int64_t)d.nb * d.in, d.in};
+    const Plan p = plan_for(d.rows, d.in, d.nb, (d.out + 63) / 64 * parts, false);
+    e = bf ? gemm<false, true, __nv_bfloat16>(a, expanded(ex, d.w()), r, nullptr, d.nb, d.out, 1, p, status, st)
+           : gemm<false, true, float>(a, expanded(ex, d.w()), r, nullptr, d.nb, d.out, 3, p, status, st);
+    if (e != cudaSuccess) return e;
+  }
+  if (dW == nullptr) return cudaSuccess;
+  if ((e = expand(x, ex, st)) != cudaSuccess) return e;
+  const Plan p = dw_plan(d);
+  const Operand ak = rows_as_k(a, d, d.out), b = expanded(ex, d.x());
+  const int64_t n = (int64_t)d.nb * d.out * d.in;
+  if (p.nsplit > 1) {
+    const Result r{part, d.out, d.in, (int64_t)d.nb * p.nsplit, d.in, (int64_t)d.out * d.in};
+    if ((e = gemm<true, true, float>(ak, b, r, nullptr, d.nb, d.rows, parts, p, status, st)) != cudaSuccess) return e;
+    return bf ? launch_kernel(mx4_sum_kernel<__nv_bfloat16>, dim3(blocks_for(n)), dim3(256), 0, st, true, (const float*)part, n, p.nsplit,
+                              (__nv_bfloat16*)dW)
+              : launch_kernel(mx4_sum_kernel<float>, dim3(blocks_for(n)), dim3(256), 0, st, true, (const float*)part, n, p.nsplit, (float*)dW);
+  }
+  const Result r{dW, d.out, d.in, d.nb, d.in, (int64_t)d.out * d.in};
+  return bf ? gemm<true, true, __nv_bfloat16>(ak, b, r, nullptr, d.nb, d.rows, 1, p, status, st)
+            : gemm<true, true, float>(ak, b, r, nullptr, d.nb, d.rows, 3, p, status, st);
+}
+
+size_t mx4_dbias_bytes(int64_t rows, int64_t cols) {
+  return (size_t)((rows + kBiasRows - 1) / kBiasRows) * (size_t)cols * 4;
+}
+cudaError_t mx4_dbias(const void* dY, int64_t rows, int64_t cols, int dtype, float* part, void* dbias,
+                      cudaStream_t st) {
+  return dtype == MONARCH_BF16 ? dbias_t<__nv_bfloat16>(dY, rows, cols, part, dbias, st)
+                               : dbias_t<float>(dY, rows, cols, part, dbias, st);
+}
+
+}  // namespace monarch

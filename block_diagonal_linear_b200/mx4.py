@@ -171,9 +171,12 @@ def _expect(dtype, **ts):
             raise ValueError("%s must be %s of shape %s, is %s of shape %s" % (name, dtype, shape, t.dtype, tuple(t.shape)))
 
 
-def mx4_linear_workspace_bytes(rows: int, nblocks: int, in_blk: int, out_blk: int, dtype="bf16", bias: bool = False) -> int:
+def mx4_linear_workspace_bytes(rows: int, nblocks: int, in_blk: int, out_blk: int, dtype="bf16", bias: bool = False,
+                               backward: bool = False) -> int:
+    """Workspace of mx4_linear_fwd with a plain X, or of mx4_linear_bwd."""
     d = MonarchMx4LinearDims(int(rows), int(nblocks), int(in_blk), int(out_blk), int(bool(bias)), dtype_code(dtype))
-    return int(lib().monarch_mx4_linear_workspace_bytes(ctypes.byref(d)))
+    f = lib().monarch_mx4_linear_bwd_workspace_bytes if backward else lib().monarch_mx4_linear_wfwd_workspace_bytes
+    return int(f(ctypes.byref(d)))
 
 
 def mx4_linear_fwd(X, W: Mx4, bias=None, Y=None, dtype=None, workspace=None, stream=None):
@@ -205,7 +208,7 @@ def mx4_linear_fwd(X, W: Mx4, bias=None, Y=None, dtype=None, workspace=None, str
               ctypes.byref(d), _p(Y))
     else:
         device = _same_device(X, W.codes, W.scales, bias, Y, workspace)
-        need = int(lib().monarch_mx4_linear_workspace_bytes(ctypes.byref(d)))
+        need = int(lib().monarch_mx4_linear_wfwd_workspace_bytes(ctypes.byref(d)))
         workspace, wp, wn = _workspace(workspace, need, device, stream)
         _call("monarch_mx4_linear_wfwd", device, stream, _p(X), _p(W.codes), _p(W.scales), _p(bias), ctypes.byref(d), _p(Y),
               wp, wn)
@@ -239,7 +242,7 @@ def mx4_linear_bwd(dY, X, W, bias: bool = False, need_dX: bool = True, dX=None, 
     if bias and dbias is None:
         dbias = _empty((n_out,), dY.dtype, device, stream)
     d = MonarchMx4LinearDims(rows, W.nblocks, W.cols, W.rows, int(bool(bias)), code)
-    need = int(lib().monarch_mx4_linear_workspace_bytes(ctypes.byref(d)))
+    need = int(lib().monarch_mx4_linear_bwd_workspace_bytes(ctypes.byref(d)))
     workspace, wp, wn = _workspace(workspace, need, device, stream)
     _call("monarch_mx4_linear_bwd", device, stream, _p(dY), _p(X.codes) if X is not None else None,
           _p(X.scales) if X is not None else None, _p(W.codes), _p(W.scales), ctypes.byref(d),

@@ -381,8 +381,11 @@ typedef struct {
   int32_t dtype;          /* monarch_dtype of X, bias, Y and the gradients              */
 } monarch_mx4_linear_dims;
 
-/* Workspace of monarch_mx4_linear_wfwd and _bwd, 256-byte aligned (0: may be NULL; 0 if ld is bad). */
-MONARCH_API size_t monarch_mx4_linear_workspace_bytes(const monarch_mx4_linear_dims* ld);
+/* Workspace of monarch_mx4_linear_wfwd and of monarch_mx4_linear_bwd, 256-byte aligned (0: may be NULL; 0
+ * if ld is bad).  It holds the MX4 operand's values in bf16 beyond 64 rows, plain operands whose rows TMA
+ * cannot address, and partial sums. */
+MONARCH_API size_t monarch_mx4_linear_wfwd_workspace_bytes(const monarch_mx4_linear_dims* ld);
+MONARCH_API size_t monarch_mx4_linear_bwd_workspace_bytes(const monarch_mx4_linear_dims* ld);
 /* Both operands in MX4. */
 MONARCH_API int monarch_mx4_linear_fwd(const void* x_codes, const void* x_scales, const void* w_codes,
                                        const void* w_scales, const void* bias, const monarch_mx4_linear_dims* ld,

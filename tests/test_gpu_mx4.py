@@ -364,7 +364,7 @@ def test_nothing_is_written_outside_the_outputs(rows, nb, inn, out):
     dW, ok2 = guarded((nb, out, inn), torch.bfloat16)
     db, ok3 = guarded((nb * out,), torch.bfloat16)
     want = bdl.mx4_linear_bwd(t["dY"], Xq, Wq, bias=True)
-    need = bdl.mx4_linear_workspace_bytes(rows, nb, inn, out, "bf16", True)
+    need = bdl.mx4_linear_workspace_bytes(rows, nb, inn, out, "bf16", True, backward=True)
     ws = torch.full((need + 512,), 9, dtype=torch.uint8, device="cuda")
     got = bdl.mx4_linear_bwd(t["dY"], Xq, Wq, bias=True, dX=dX, dW=dW, dbias=db, workspace=ws[:need])
     assert all(torch.equal(a, b) for a, b in zip(got, want)) and ok1() and ok2() and ok3()

@@ -118,7 +118,7 @@ def test_linear_refusals():
         return L.monarch_mx4_linear_fwd(xc, xs, wc, ws, b, ctypes.byref(d) if d is not None else None, Y, None)
 
     def w(d, X=at(0), wc=at(2), ws=at(3), b=at(4), Y=at(5), work=at(6), n=None):
-        n = L.monarch_mx4_linear_workspace_bytes(ctypes.byref(d)) if n is None and d is not None else n or 0
+        n = L.monarch_mx4_linear_wfwd_workspace_bytes(ctypes.byref(d)) if n is None and d is not None else n or 0
         return L.monarch_mx4_linear_wfwd(X, wc, ws, b, ctypes.byref(d) if d is not None else None, Y, work, n, None)
 
     good = D(40, 2, 64, 96, 1, bdl.MONARCH_BF16)
@@ -127,7 +127,8 @@ def test_linear_refusals():
         assert g(D(40, 2, 64, 96, 0, 5)) == CODES["MONARCH_ERR_DTYPE"]
         for bad in (D(-1, 2, 64, 96, 0, 0), D(4, 0, 64, 96, 0, 0), D(4, 2, 0, 96, 0, 0), D(4, 2, 64, -3, 0, 0)):
             assert g(bad) == CODES["MONARCH_ERR_DIMS"]
-            assert L.monarch_mx4_linear_workspace_bytes(ctypes.byref(bad)) == 0
+            assert L.monarch_mx4_linear_wfwd_workspace_bytes(ctypes.byref(bad)) == 0
+            assert L.monarch_mx4_linear_bwd_workspace_bytes(ctypes.byref(bad)) == 0
         assert g(D(4, 2, 64, 2 ** 20 + 1, 0, 0)) == CODES["MONARCH_ERR_UNSUPPORTED"]
         for name in ("wc", "ws", "b", "Y"):
             assert g(good, **{name: None}) == CODES["MONARCH_ERR_NULL"]
@@ -135,6 +136,12 @@ def test_linear_refusals():
         assert g(good, Y=P((3 << 40) + 32)) == CODES["MONARCH_ERR_ALIAS"]      # W's codes
         assert g(good, Y=P((5 << 40) - 16)) == CODES["MONARCH_ERR_ALIAS"]      # into the bias
         assert g(D(0, 2, 64, 96, 1, 1), wc=None, ws=None, b=None, Y=None) == 0
+    long = D(65, 2, 64, 96, 1, bdl.MONARCH_BF16)   # beyond 64 rows the weight's values are expanded in a workspace
+    need = L.monarch_mx4_linear_wfwd_workspace_bytes(ctypes.byref(long))
+    assert need > 0 and L.monarch_mx4_linear_wfwd_workspace_bytes(ctypes.byref(good)) == 0
+    assert w(long, work=None) == w(long, n=need - 1) == CODES["MONARCH_ERR_WORKSPACE"]
+    assert w(long, work=P((7 << 40) + 16)) == CODES["MONARCH_ERR_ALIGN"]
+    assert w(long, work=at(0)) == w(long, work=at(2)) == w(long, work=at(5)) == CODES["MONARCH_ERR_ALIAS"]
     assert f(good, xc=None) == f(good, xs=None) == w(good, X=None) == CODES["MONARCH_ERR_NULL"]
     assert f(good, xc=P(8)) == f(good, xs=P(8)) == w(good, X=P(8)) == CODES["MONARCH_ERR_ALIGN"]
 
@@ -143,7 +150,7 @@ def test_linear_backward_refusals():
     L = bdl.lib()
     D = bdl.MonarchMx4LinearDims
     good = D(40, 2, 64, 96, 1, bdl.MONARCH_BF16)
-    need = L.monarch_mx4_linear_workspace_bytes(ctypes.byref(good))
+    need = L.monarch_mx4_linear_bwd_workspace_bytes(ctypes.byref(good))
     assert need > 0
 
     def g(d=good, dY=at(0), xc=at(1), xs=at(2), wc=at(3), ws=at(4), dX=at(5), dW=at(6), db=at(7), work=at(8), n=need):
