@@ -17,8 +17,12 @@ import ctypes
 
 import torch
 
-from . import (MONARCH_BF16, MonarchDims, MonarchMx4Dims, MonarchMx4LinearDims, _check, _check_tensors, _require_cuda,
-               _torch_dtype, dtype_code, lib)
+from . import MONARCH_BF16, MONARCH_F32, MonarchDims, MonarchMx4Dims, MonarchMx4LinearDims, _check, dtype_code, lib
+
+_DTYPES = {MONARCH_BF16: torch.bfloat16, MONARCH_F32: torch.float32}
+_CODES = {torch.bfloat16: MONARCH_BF16, torch.float32: MONARCH_F32}
+_byref = ctypes.byref
+_raw_stream = torch._C._cuda_getCurrentRawStream  # address of a device's current stream
 
 
 class Mx4:
@@ -28,16 +32,20 @@ class Mx4:
     ``by_block`` says which plain layout it came from: (nblocks, rows, cols), or (rows, nblocks * cols);
     ``dtype`` is that tensor's type ("bf16" / "f32")."""
 
-    __slots__ = ("codes", "scales", "rows", "nblocks", "cols", "by_block", "dtype")
+    __slots__ = ("codes", "scales", "rows", "nblocks", "cols", "by_block", "code")
 
     def __init__(self, codes, scales, rows: int, nblocks: int, cols: int, by_block: bool, dtype):
         self.rows, self.nblocks, self.cols, self.by_block = int(rows), int(nblocks), int(cols), bool(by_block)
-        self.dtype = "bf16" if dtype_code(dtype) == MONARCH_BF16 else "f32"
+        self.code = dtype_code(dtype)
         self.codes, self.scales = codes, scales
-        need = _buffer_bytes(_dims(self, self.dtype))
+        need = _buffer_bytes(_dims(self, self.code))
         for name, t, n in (("codes", codes, need[0]), ("scales", scales, need[1])):
             if t.dtype != torch.uint8 or t.numel() != n:
                 raise ValueError("%s must be uint8 with %d elements" % (name, n))
+
+    @property
+    def dtype(self) -> str:
+        return "bf16" if self.code == MONARCH_BF16 else "f32"
 
     @property
     def device(self):
@@ -56,70 +64,82 @@ class Mx4:
         return "Mx4(shape=%s, nblocks=%d, dtype=%s)" % (tuple(self.shape), self.nblocks, self.dtype)
 
 
-def _dims(q, dtype) -> MonarchMx4Dims:
-    return MonarchMx4Dims(q.rows, q.nblocks, q.cols, int(q.by_block), dtype_code(dtype))
+def _dims(q, code: int) -> MonarchMx4Dims:
+    return MonarchMx4Dims(q.rows, q.nblocks, q.cols, q.by_block, code)
 
 
 def _buffer_bytes(d) -> tuple:
     """(codes, scales) bytes; raises MonarchError on sizes that the library does not take."""
-    L, p = lib(), ctypes.byref(d)
-    codes, scales = int(L.monarch_mx4_code_bytes(p)), int(L.monarch_mx4_scale_bytes(p))
+    L, p = lib(), _byref(d)
+    codes, scales = L.monarch_mx4_code_bytes(p), L.monarch_mx4_scale_bytes(p)
     if codes == 0 and d.rows != 0:
         _check("monarch_mx4_quantise", L.monarch_mx4_quantise(None, p, None, None, None))
     return codes, scales
 
 
-def _same_device(*ts):
-    """Contiguous CUDA tensors of one device; returns it."""
-    _require_cuda(*ts)
+# The binding's own cost counts where a kernel takes a few microseconds (a decoding step), so the checks
+# below use one call per property and no object that is not needed.
+def _device(*ts) -> int:
+    """Index of the device that holds every tensor; all must be contiguous CUDA tensors."""
     device = None
     for t in ts:
         if t is not None:
+            i = t.get_device()
+            if i < 0 or not t.is_contiguous():
+                raise ValueError("Monarch kernels take contiguous CUDA tensors")
             if device is None:
-                device = t.device
-            elif t.device != device:
-                raise ValueError("tensors on %s and %s: one call takes one device's" % (device, t.device))
+                device = i
+            elif i != device:
+                raise ValueError("tensors on cuda:%d and cuda:%d: one call takes one device's" % (device, i))
     return device
 
 
-def _empty(shape, dtype, device, stream):
-    """Memory for work on `stream` (None: the device's current one)."""
+def _empty(like, shape, dtype, stream):
+    """Memory on like's device for work on `stream` (None: that device's current one)."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
 
 
-def _call(name, device, stream, *args):
-    """The C entry point `name` with args and the stream handle, `device` being the current one."""
-    fn = getattr(lib(), name)
-    s = ctypes.c_void_p((torch.cuda.current_stream(device) if stream is None else stream).cuda_stream)
-    if device.index == torch.cuda.current_device():
+def _call(name, fn, device, stream, *args):
+    """fn, the C entry point `name`, on args and the stream handle, with `device` the current one."""
+    s = _raw_stream(device) if stream is None else stream.cuda_stream
+    if device == torch.cuda.current_device():
         rc = fn(*args, s)
     else:
         with torch.cuda.device(device):
             rc = fn(*args, s)
-    _check(name, rc)
+    if rc:
+        _check(name, rc)
 
 
 def _p(t):
     return None if t is None else t.data_ptr()
 
 
-def _workspace(workspace, need, device, stream):
+def _workspace(workspace, need, like, stream):
     """(tensor to keep alive, address, bytes) of the caller's workspace, or of a new one."""
     if workspace is None:
         if need == 0:
             return None, None, 0
-        workspace = _empty(need, torch.uint8, device, stream)
+        workspace = _empty(like, (need,), torch.uint8, stream)
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _code(t, name) -> int:
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise ValueError("%s is %s: bfloat16 and float32 are taken" % (name, t.dtype))
+    return code
 
 
 def mx4_quantise(X, nblocks: int | None = None, stream=None) -> Mx4:
     """X in MX4.  A 3-D X is a weight (nblocks, out_blk, in_blk); a 2-D X (rows, nblocks * cols) holds
     activations of `nblocks` blocks (default 1).  Scales never span two rows or two blocks."""
-    code = dtype_code(X.dtype)
-    if X.dim() == 3:
+    code = _code(X, "X")
+    by_block = X.dim() == 3
+    if by_block:
         nb, rows, cols = X.shape
         if nblocks is not None and nblocks != nb:
             raise ValueError("X has %d blocks, nblocks is %d" % (nb, nblocks))
@@ -131,27 +151,28 @@ def mx4_quantise(X, nblocks: int | None = None, stream=None) -> Mx4:
         cols = width // nb
     else:
         raise ValueError("X must have 2 or 3 dimensions, got %d" % X.dim())
-    device = _same_device(X)
-    d = MonarchMx4Dims(rows, nb, cols, int(X.dim() == 3), code)
+    device = _device(X)
+    d = MonarchMx4Dims(rows, nb, cols, by_block, code)
     nc, ns = _buffer_bytes(d)
     q = Mx4.__new__(Mx4)
-    q.codes, q.scales = _empty(nc, torch.uint8, device, stream), _empty(ns, torch.uint8, device, stream)
-    q.rows, q.nblocks, q.cols, q.by_block = rows, nb, cols, X.dim() == 3
-    q.dtype = "bf16" if code == MONARCH_BF16 else "f32"
-    _call("monarch_mx4_quantise", device, stream, _p(X), ctypes.byref(d), _p(q.codes), _p(q.scales))
+    q.codes, q.scales = _empty(X, (nc,), torch.uint8, stream), _empty(X, (ns,), torch.uint8, stream)
+    q.rows, q.nblocks, q.cols, q.by_block, q.code = rows, nb, cols, by_block, code
+    _call("monarch_mx4_quantise", lib().monarch_mx4_quantise, device, stream, X.data_ptr(), _byref(d), q.codes.data_ptr(),
+          q.scales.data_ptr())
     return q
 
 
 def mx4_dequantise(q: Mx4, dtype=None, out=None, stream=None):
     """The values of q in the layout it came from, in `dtype` (default: the type it came in)."""
-    code = dtype_code(q.dtype if dtype is None else dtype)
-    dt = _torch_dtype(code)
+    code = q.code if dtype is None else dtype_code(dtype)
+    dt = _DTYPES[code]
     if out is None:
-        out = _empty(q.shape, dt, q.device, stream)
+        out = _empty(q.codes, q.shape, dt, stream)
     elif tuple(out.shape) != tuple(q.shape) or out.dtype != dt:
         raise ValueError("out must be %s of shape %s" % (dt, tuple(q.shape)))
-    device = _same_device(q.codes, q.scales, out)
-    _call("monarch_mx4_dequantise", device, stream, _p(q.codes), _p(q.scales), ctypes.byref(_dims(q, code)), _p(out))
+    device = _device(q.codes, q.scales, out)
+    _call("monarch_mx4_dequantise", lib().monarch_mx4_dequantise, device, stream, q.codes.data_ptr(), q.scales.data_ptr(),
+          _byref(_dims(q, code)), out.data_ptr())
     return out
 
 
@@ -165,10 +186,9 @@ def _activations(X, W):
         raise ValueError("X is %r, W %r: an Mx4 X must hold activations with W's blocks" % (X, W))
 
 
-def _expect(dtype, **ts):
-    for name, (t, shape) in ts.items():
-        if t is not None and (tuple(t.shape) != shape or t.dtype != dtype):
-            raise ValueError("%s must be %s of shape %s, is %s of shape %s" % (name, dtype, shape, t.dtype, tuple(t.shape)))
+def _expect(t, name, shape, dtype):
+    if t is not None and (t.shape != shape or t.dtype != dtype):
+        raise ValueError("%s must be %s of shape %s, is %s of shape %s" % (name, dtype, shape, t.dtype, tuple(t.shape)))
 
 
 def mx4_linear_workspace_bytes(rows: int, nblocks: int, in_blk: int, out_blk: int, dtype="bf16", bias: bool = False,
@@ -188,30 +208,32 @@ def mx4_linear_fwd(X, W: Mx4, bias=None, Y=None, dtype=None, workspace=None, str
     both = isinstance(X, Mx4)
     if both:
         _activations(X, W)
-        code = dtype_code(X.dtype if dtype is None else dtype)
+        code = X.code if dtype is None else dtype_code(dtype)
         rows = X.rows
     else:
-        code = dtype_code(X.dtype)
+        code = _code(X, "X")
         if dtype is not None and dtype_code(dtype) != code:
             raise ValueError("dtype is X's unless X is an Mx4")
         rows = X.shape[0]
-        _expect(X.dtype, X=(X, (rows, W.nblocks * W.cols)))
-    dt = _torch_dtype(code)
+        _expect(X, "X", (rows, W.nblocks * W.cols), X.dtype)
+    dt = _DTYPES[code]
     n_out = W.nblocks * W.rows
-    _expect(dt, bias=(bias, (n_out,)), Y=(Y, (rows, n_out)))
+    _expect(bias, "bias", (n_out,), dt)
     if Y is None:
-        Y = _empty((rows, n_out), dt, W.device, stream)
-    d = MonarchMx4LinearDims(rows, W.nblocks, W.cols, W.rows, int(bias is not None), code)
-    if both:
-        device = _same_device(X.codes, X.scales, W.codes, W.scales, bias, Y)
-        _call("monarch_mx4_linear_fwd", device, stream, _p(X.codes), _p(X.scales), _p(W.codes), _p(W.scales), _p(bias),
-              ctypes.byref(d), _p(Y))
+        Y = _empty(W.codes, (rows, n_out), dt, stream)
     else:
-        device = _same_device(X, W.codes, W.scales, bias, Y, workspace)
-        need = int(lib().monarch_mx4_linear_wfwd_workspace_bytes(ctypes.byref(d)))
-        workspace, wp, wn = _workspace(workspace, need, device, stream)
-        _call("monarch_mx4_linear_wfwd", device, stream, _p(X), _p(W.codes), _p(W.scales), _p(bias), ctypes.byref(d), _p(Y),
-              wp, wn)
+        _expect(Y, "Y", (rows, n_out), dt)
+    d = _byref(MonarchMx4LinearDims(rows, W.nblocks, W.cols, W.rows, bias is not None, code))
+    L = lib()
+    if both:
+        device = _device(X.codes, X.scales, W.codes, W.scales, bias, Y)
+        _call("monarch_mx4_linear_fwd", L.monarch_mx4_linear_fwd, device, stream, X.codes.data_ptr(), X.scales.data_ptr(),
+              W.codes.data_ptr(), W.scales.data_ptr(), _p(bias), d, Y.data_ptr())
+    else:
+        device = _device(X, W.codes, W.scales, bias, Y, workspace)
+        workspace, wp, wn = _workspace(workspace, L.monarch_mx4_linear_wfwd_workspace_bytes(d), X, stream)
+        _call("monarch_mx4_linear_wfwd", L.monarch_mx4_linear_wfwd, device, stream, X.data_ptr(), W.codes.data_ptr(),
+              W.scales.data_ptr(), _p(bias), d, Y.data_ptr(), wp, wn)
     return Y
 
 
@@ -221,7 +243,8 @@ def mx4_linear_bwd(dY, X, W, bias: bool = False, need_dX: bool = True, dX=None, 
     to the tensors X and W were rounded from.  X = None (a frozen layer) leaves out dW; need_dX = False
     leaves out dX; dbias is None without `bias`."""
     _weight(W)
-    code = dtype_code(dY.dtype)
+    code = _code(dY, "dY")
+    dt = dY.dtype
     rows = dY.shape[0]
     n_in, n_out = W.nblocks * W.cols, W.nblocks * W.rows
     if X is not None:
@@ -232,42 +255,50 @@ def mx4_linear_bwd(dY, X, W, bias: bool = False, need_dX: bool = True, dX=None, 
             raise ValueError("X has %d rows, dY %d" % (X.rows, rows))
     elif dW is not None:
         raise ValueError("dW needs X")
-    _expect(dY.dtype, dY=(dY, (rows, n_out)), dX=(dX, (rows, n_in)), dW=(dW, (W.nblocks, W.rows, W.cols)),
-            dbias=(dbias, (n_out,)))
-    device = _same_device(dY, W.codes, W.scales, dX, dW, dbias, workspace, *((X.codes, X.scales) if X is not None else ()))
-    if need_dX and dX is None:
-        dX = _empty((rows, n_in), dY.dtype, device, stream)
+    _expect(dY, "dY", (rows, n_out), dt)
+    _expect(dX, "dX", (rows, n_in), dt)
+    _expect(dW, "dW", (W.nblocks, W.rows, W.cols), dt)
+    _expect(dbias, "dbias", (n_out,), dt)
+    if not need_dX:
+        dX = None
+    elif dX is None:
+        dX = _empty(dY, (rows, n_in), dt, stream)
     if X is not None and dW is None:
-        dW = _empty((W.nblocks, W.rows, W.cols), dY.dtype, device, stream)
-    if bias and dbias is None:
-        dbias = _empty((n_out,), dY.dtype, device, stream)
-    d = MonarchMx4LinearDims(rows, W.nblocks, W.cols, W.rows, int(bool(bias)), code)
-    need = int(lib().monarch_mx4_linear_bwd_workspace_bytes(ctypes.byref(d)))
-    workspace, wp, wn = _workspace(workspace, need, device, stream)
-    _call("monarch_mx4_linear_bwd", device, stream, _p(dY), _p(X.codes) if X is not None else None,
-          _p(X.scales) if X is not None else None, _p(W.codes), _p(W.scales), ctypes.byref(d),
-          _p(dX) if need_dX else None, _p(dW), _p(dbias) if bias else None, wp, wn)
-    return dX if need_dX else None, dW, dbias if bias else None
+        dW = _empty(dY, (W.nblocks, W.rows, W.cols), dt, stream)
+    if not bias:
+        dbias = None
+    elif dbias is None:
+        dbias = _empty(dY, (n_out,), dt, stream)
+    xc, xs = (X.codes, X.scales) if X is not None else (None, None)
+    device = _device(dY, W.codes, W.scales, xc, xs, dX, dW, dbias, workspace)
+    d = _byref(MonarchMx4LinearDims(rows, W.nblocks, W.cols, W.rows, bool(bias), code))
+    L = lib()
+    workspace, wp, wn = _workspace(workspace, L.monarch_mx4_linear_bwd_workspace_bytes(d), dY, stream)
+    _call("monarch_mx4_linear_bwd", L.monarch_mx4_linear_bwd, device, stream, dY.data_ptr(), _p(xc), _p(xs), W.codes.data_ptr(),
+          W.scales.data_ptr(), d, _p(dX), _p(dW), _p(dbias), wp, wn)
+    return dX, dW, dbias
 
 
 def mx4_fwd(X, R: Mx4, L: Mx4, shape: dict, Y=None, workspace=None, stream=None):
     """Monarch map Y = X M^T with both factors in MX4 (fwd() with the factors' quantised values)."""
     _weight(R, "R")
     _weight(L, "L")
-    for name, q, want in (("R", R, (shape["nb1"], shape["out1"], shape["in1"])),
-                          ("L", L, (shape["nb2"], shape["out2"], shape["in2"]))):
-        if tuple(q.shape) != tuple(want):
-            raise ValueError("%s has shape %s, the dims need %s" % (name, tuple(q.shape), tuple(want)))
-    code = dtype_code(X.dtype)
+    nb1, in1, out1, nb2, in2, out2 = shape["nb1"], shape["in1"], shape["out1"], shape["nb2"], shape["in2"], shape["out2"]
+    for name, q, want in (("R", R, (nb1, out1, in1)), ("L", L, (nb2, out2, in2))):
+        if q.shape != want:
+            raise ValueError("%s has shape %s, the dims need %s" % (name, q.shape, want))
+    code = _code(X, "X")
+    dt = X.dtype
     rows = X.shape[0]
-    _check_tensors(shape, rows, X.dtype, X=X, Y=Y)
+    _expect(X, "X", (rows, nb1 * in1), dt)
     if Y is None:
-        Y = _empty((rows, shape["nb2"] * shape["out2"]), X.dtype, X.device, stream)
-    d = MonarchDims(rows, shape["nb1"], shape["in1"], shape["out1"], shape["nb2"], shape["in2"], shape["out2"],
-                    int(shape.get("out_transpose", 1)), code)
-    device = _same_device(X, R.codes, R.scales, L.codes, L.scales, Y, workspace)
-    need = int(lib().monarch_mx4_fwd_workspace_bytes(ctypes.byref(d)))
-    workspace, wp, wn = _workspace(workspace, need, device, stream)
-    _call("monarch_mx4_fwd", device, stream, _p(X), _p(R.codes), _p(R.scales), _p(L.codes), _p(L.scales), ctypes.byref(d),
-          _p(Y), wp, wn)
+        Y = _empty(X, (rows, nb2 * out2), dt, stream)
+    else:
+        _expect(Y, "Y", (rows, nb2 * out2), dt)
+    d = _byref(MonarchDims(rows, nb1, in1, out1, nb2, in2, out2, int(shape.get("out_transpose", 1)), code))
+    lb = lib()
+    device = _device(X, R.codes, R.scales, L.codes, L.scales, Y, workspace)
+    workspace, wp, wn = _workspace(workspace, lb.monarch_mx4_fwd_workspace_bytes(d), X, stream)
+    _call("monarch_mx4_fwd", lb.monarch_mx4_fwd, device, stream, X.data_ptr(), R.codes.data_ptr(), R.scales.data_ptr(),
+          L.codes.data_ptr(), L.scales.data_ptr(), d, Y.data_ptr(), wp, wn)
     return Y

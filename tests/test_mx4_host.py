@@ -214,7 +214,7 @@ def test_binding_refuses_wrong_tensors():
         bdl.mx4_quantise(torch.zeros(4))
     with pytest.raises(ValueError):
         bdl.mx4_quantise(torch.zeros(3, 4, 4), nblocks=2)
-    with pytest.raises(KeyError):
+    with pytest.raises(ValueError):
         bdl.mx4_quantise(torch.zeros(4, 4, dtype=torch.float16))
     with pytest.raises(ValueError):
         bdl.Mx4(W.codes[1:], W.scales, 96, 2, 64, True, "bf16")
