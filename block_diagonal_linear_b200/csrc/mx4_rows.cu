@@ -1,6 +1,6 @@
 // Few tokens through an MX4 weight:  Y(r; b, o) = sum_i X[r][b*in + i] W^[b][o][i] (+ bias), X as it is.
 //
-// A decoding step reads the whole weight for a handful of tokens, so the kernel is bound by the
+// A decoding step reads the whole weight for a handful of tokens, so the kernels are bound by the
 // latency and bandwidth of that one read (17/32 bytes a weight).  The product runs on mma.sync
 // m16n8k16 with the weights as the 16-row operand and 8 tokens as the columns: codes become bf16
 // values in registers (exact), X enters as one bf16 part, or, in fp32, as 2 or 3 parts that are cut
@@ -8,10 +8,16 @@
 //
 // A warp takes 16 outputs and walks scale tiles of 128 inputs: a lane holds one whole scale block of
 // two outputs (16 bytes of codes each), so that one multiplier serves all of a lane's values; which
-// input stands where inside an MMA does not matter as long as both operands agree.  The 16 outputs
-// are 4 neighbours in each of the 4 column groups of a scale tile, whose scale words are contiguous.
-// Warps of a CTA split the inputs (up to 8 ways) and then outputs; their sums join in shared memory
-// in a fixed order.  Every lane asks for up to four scale tiles before it uses the first.
+// input stands where inside an MMA does not matter as long as both operands agree.  Every lane asks for
+// up to four scale tiles of codes before it uses the first.  The inputs are split up to 8 ways, and the
+// shares' sums join in a fixed order.
+//
+// Up to 8 bf16 tokens (mx4_token_kernel) the shares are warps of a CTA and a lane reads its inputs where
+// they are: the weight is all there is to read.  More tokens, or fp32 ones (mx4_batch_kernel, up to 64 a
+// pass), would have every warp gather and cut its own inputs again, 16 bytes from 16 lines a load (4096 ->
+// 4096: 18.5 us for 32 bf16 tokens against 12.0, 14.8 for one in fp32); there the shares are CTAs of a
+// cluster, and a CTA's 8 warps take 128 outputs and share one copy of the inputs in shared memory, already
+// cut into parts, in the order in which lanes read it.
 #include "mx4.cuh"
 #include "tc_common.cuh"
 
@@ -20,7 +26,6 @@ namespace monarch {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kAhead = 4;  // scale tiles in flight
 
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -87,153 +92,335 @@ __device__ __forceinline__ void split8(const uint32_t (&x)[8], uint32_t (&b)[PAR
   }
 }
 
-template <typename TX, int PARTS, typename TY, bool VEC, int NT>
-__global__ void __launch_bounds__(kWarps * 32)
-    mx4_rows_kernel(const TX* X, Mx4View w, int64_t rows, Mx4Out o, const TY* bias, TY* Y, int wk, bool w_early) {
-  __shared__ float part[kWarps][16][8 * NT + 1];
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-  const int kw = warp % wk, mw = warp / wk;  // this warp's share of the inputs, and its 16 outputs
-  const int b = blockIdx.y;
-  const int64_t r0 = (int64_t)blockIdx.z * (8 * NT);
-  const int64_t mt = (int64_t)blockIdx.x * (kWarps / wk) + mw;  // 8 of them in 128 outputs
-  // MMA row m = 4i + j is output 128*(mt/8) + 4*(mt%8) + i + 32*j
-  const int64_t o0 = (mt >> 3) * 128 + (mt & 7) * 4 + (g >> 2) + 32 * (g & 3), o1 = o0 + 2;
-  const int katoms = w.s.katoms(), kblocks = w.s.kblocks();
-  const int64_t ratom = mt >> 3;
-  const bool in_range = ratom < w.s.ratoms();
-  const uint8_t* c0 = w.codes + w.s.code_row(b, o0) + t * 16;
-  const uint8_t* c1 = w.codes + w.s.code_row(b, o1) + t * 16;
-  const uint8_t* sc = w.scales + ((((int64_t)b * w.s.ratoms() + ratom) * katoms) << 9) + (((mt & 7) * 4 + (g >> 2)) << 4) + ((g & 3) << 2);
-  const int64_t pitch = (int64_t)w.s.nblocks * w.s.cols;
-
-  float acc[NT][4] = {};
-  uint4 q0[kAhead], q1[kAhead];
-  uint32_t s0[kAhead], s1[kAhead];
-  auto fetch = [&](int ka0) {  // this warp's next kAhead scale tiles: ka0, ka0 + wk, ...
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int ka = ka0 + i * wk;
-      const bool ok = in_range && ka < katoms && ka * 4 + t < kblocks;
-      q0[i] = ok && o0 < w.s.rows ? *(const uint4*)(c0 + (int64_t)ka * 64) : make_uint4(0, 0, 0, 0);
-      q1[i] = ok && o1 < w.s.rows ? *(const uint4*)(c1 + (int64_t)ka * 64) : make_uint4(0, 0, 0, 0);
-      s0[i] = ok ? *(const uint32_t*)(sc + (int64_t)ka * 512) : 0u;
-      s1[i] = ok ? *(const uint32_t*)(sc + (int64_t)ka * 512 + 32) : 0u;
-    }
-  };
-  // weights that no kernel of this stream is still writing may be asked for ahead of the wait
-  if (w_early) {
-    fetch(kw);
-    ptx::griddep_wait();
-  } else {
-    ptx::griddep_wait();
-    fetch(kw);
+// One scale tile's codes of a lane: 32 codes of two outputs and their scale words.
+struct Codes {
+  uint4 q0, q1;
+  uint32_t s0, s1;
+};
+struct CodeRows {  // a lane's two outputs, g and g + 8 of the warp's sixteen
+  const uint8_t *c0, *c1, *s0, *s1;
+  bool in0, in1;
+  int katoms, kblocks, t;
+  __device__ CodeRows(const Mx4View& w, int b, int64_t o, int t_) : t(t_) {
+    in0 = o < w.s.rows;
+    in1 = o + 8 < w.s.rows;
+    katoms = w.s.katoms();
+    kblocks = w.s.kblocks();
+    c0 = w.codes + w.s.code_row(b, o) + t * 16;
+    c1 = w.codes + w.s.code_row(b, o + 8) + t * 16;
+    s0 = w.scales + w.s.scale_at(b, o, 0);
+    s1 = w.scales + w.s.scale_at(b, o + 8, 0);
   }
-  ptx::griddep_launch_dependents();
-
-  for (int ka0 = kw; ka0 < katoms; ka0 += kAhead * wk) {
-    if (ka0 != kw) fetch(ka0);
+  __device__ __forceinline__ Codes at(int ka) const {
+    const bool ok = ka < katoms && ka * 4 + t < kblocks;
+    Codes c;
+    c.q0 = ok && in0 ? *(const uint4*)(c0 + (int64_t)ka * 64) : make_uint4(0, 0, 0, 0);
+    c.q1 = ok && in1 ? *(const uint4*)(c1 + (int64_t)ka * 64) : make_uint4(0, 0, 0, 0);
+    c.s0 = ok && in0 ? *(const uint32_t*)(s0 + (int64_t)ka * 512) : 0u;
+    c.s1 = ok && in1 ? *(const uint32_t*)(s1 + (int64_t)ka * 512) : 0u;
+    return c;
+  }
+};
+// Codes to bf16 values: word v's pair (j, j + 4) at 4v + j.  spread8 leaves value / 2^126; scales up to 2^1
+// fold into one multiplication, larger ones and NaN take a second.
+__device__ __forceinline__ void values(const Codes& c, int t, uint32_t (&a0)[16], uint32_t (&a1)[16]) {
+  const uint32_t e0 = (c.s0 >> (8 * t)) & 255u, e1 = (c.s1 >> (8 * t)) & 255u;
+  const bool big = e0 > 128u || e1 > 128u;
+  const uint32_t f0 = (e0 > 128u ? 253u : e0 + 126u) * 0x00800080u, f1 = (e1 > 128u ? 253u : e1 + 126u) * 0x00800080u;
+  const uint32_t w0[4] = {c.q0.x, c.q0.y, c.q0.z, c.q0.w}, w1[4] = {c.q1.x, c.q1.y, c.q1.z, c.q1.w};
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int ka = ka0 + i * wk;
-      if (ka >= katoms) break;
-      // codes -> bf16: spread8 leaves value / 2^126; scales up to 2^1 fold into one multiplication
-      const uint32_t e0 = (s0[i] >> (8 * t)) & 255u, e1 = (s1[i] >> (8 * t)) & 255u;
-      const bool big = e0 > 128u || e1 > 128u;
-      const uint32_t f0 = (e0 > 128u ? 253u : e0 + 126u) * 0x00800080u, f1 = (e1 > 128u ? 253u : e1 + 126u) * 0x00800080u;
-      uint32_t a0[16], a1[16];  // word v's pair j at 4v + j
-      const uint32_t w0[4] = {q0[i].x, q0[i].y, q0[i].z, q0[i].w}, w1[4] = {q1[i].x, q1[i].y, q1[i].z, q1[i].w};
+  for (int v = 0; v < 4; ++v) {
+    uint32_t p0[4], p1[4];
+    mx4::spread8(w0[v], p0);
+    mx4::spread8(w1[v], p1);
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        uint32_t p0[4], p1[4];
-        mx4::spread8(w0[v], p0);
-        mx4::spread8(w1[v], p1);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          a0[4 * v + j] = mul_bf16x2(p0[j], f0);
-          a1[4 * v + j] = mul_bf16x2(p1[j], f1);
-        }
-      }
-      if (__any_sync(0xffffffffu, big)) {  // 2^(byte - 127) itself, and NaN
-        const uint32_t h0 = e0 > 128u ? (e0 == 255u ? 0x7fc07fc0u : e0 * 0x00800080u) : 0x3f803f80u;
-        const uint32_t h1 = e1 > 128u ? (e1 == 255u ? 0x7fc07fc0u : e1 * 0x00800080u) : 0x3f803f80u;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          a0[j] = mul_bf16x2(a0[j], h0);
-          a1[j] = mul_bf16x2(a1[j], h1);
-        }
-      }
-      const int k = ka * 128 + t * 32;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int64_t r = r0 + n * 8 + g;
-        const TX* p = X + r * pitch + (int64_t)b * w.s.cols + k;
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          uint32_t x[8], bp[PARTS][4];
-          load8<VEC>(p + 8 * v, r < rows ? w.s.cols - k - 8 * v : 0, x);
-          split8<PARTS>(x, bp, (const TX*)nullptr);
-          // mma.sync cuts its sums off (2^-23 a step, always towards zero): an fp32 result takes them in
-          // runs of 32 inputs and joins the runs with rounded additions (4096 inputs: 1.3e-6 off without)
-          float run[4] = {};
-          float(&sum)[4] = PARTS == 3 ? run : acc[n];
-#pragma unroll
-          for (int q = PARTS - 1; q >= 0; --q) {
-            mma_16816(sum, a0[4 * v], a1[4 * v], a0[4 * v + 1], a1[4 * v + 1], bp[q][0], bp[q][1]);
-            mma_16816(sum, a0[4 * v + 2], a1[4 * v + 2], a0[4 * v + 3], a1[4 * v + 3], bp[q][2], bp[q][3]);
-          }
-          if (PARTS == 3) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[n][e] += run[e];
-          }
-        }
-      }
+    for (int j = 0; j < 4; ++j) {
+      a0[4 * v + j] = mul_bf16x2(p0[j], f0);
+      a1[4 * v + j] = mul_bf16x2(p1[j], f1);
     }
   }
+  if (__any_sync(0xffffffffu, big)) {  // 2^(byte - 127) itself, and NaN
+    const uint32_t h0 = e0 > 128u ? (e0 == 255u ? 0x7fc07fc0u : e0 * 0x00800080u) : 0x3f803f80u;
+    const uint32_t h1 = e1 > 128u ? (e1 == 255u ? 0x7fc07fc0u : e1 * 0x00800080u) : 0x3f803f80u;
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
+    for (int j = 0; j < 16; ++j) {
+      a0[j] = mul_bf16x2(a0[j], h0);
+      a1[j] = mul_bf16x2(a1[j], h1);
+    }
+  }
+}
+// acc += the 32 inputs' products of word v.  mma.sync cuts its sums off (2^-23 a step, always towards
+// zero): an fp32 result (3 parts) takes them in runs of 32 inputs and joins the runs with rounded
+// additions (4096 inputs: 1.3e-6 off without, 1e-7 with).
+template <int PARTS>
+__device__ __forceinline__ void product(float (&acc)[4], const uint32_t (&a0)[16], const uint32_t (&a1)[16], int v,
+                                        const uint32_t (&bp)[PARTS][4]) {
+  float run[4] = {};
+  float(&sum)[4] = PARTS == 3 ? run : acc;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) part[warp][g + 8 * (e >> 1)][n * 8 + 2 * t + (e & 1)] = acc[n][e];
-  __syncthreads();
-  // join the input shares in order; consecutive threads take consecutive outputs of one token
-  const int mtiles = kWarps / wk;
-  for (int e = threadIdx.x; e < mtiles * 16 * 8 * NT; e += kWarps * 32) {
-    const int m = e % 16, tile = (e / 16) % mtiles, n = e / (16 * mtiles);
-    const int64_t tt = (int64_t)blockIdx.x * mtiles + tile;
-    // row order that walks the outputs: four neighbours, then the next group of 32
-    const int64_t out = (tt >> 3) * 128 + (tt & 7) * 4 + (m & 3) + 32 * (m >> 2);
-    const int row = 4 * (m & 3) + (m >> 2);
-    if (out >= w.s.rows || r0 + n >= rows) continue;
-    float v = 0.f;
-    for (int k = 0; k < wk; ++k) v += part[tile * wk + k][row][n];
-    if (bias != nullptr) v += mx4::load(bias + (int64_t)b * w.s.rows + out);
-    st_from_f32(Y + o.at(b, r0 + n, out), v);
+  for (int q = PARTS - 1; q >= 0; --q) {
+    mma_16816(sum, a0[4 * v], a1[4 * v], a0[4 * v + 1], a1[4 * v + 1], bp[q][0], bp[q][1]);
+    mma_16816(sum, a0[4 * v + 2], a1[4 * v + 2], a0[4 * v + 3], a1[4 * v + 3], bp[q][2], bp[q][3]);
+  }
+  if (PARTS == 3) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] += run[e];
   }
 }
 
+constexpr int kAhead = 4;  // scale tiles of codes in flight
+
+template <typename TY, bool VEC>
+__global__ void __launch_bounds__(kWarps * 32)
+    mx4_token_kernel(const __nv_bfloat16* X, Mx4View w, int64_t rows, Mx4Out o, const TY* bias, TY* Y, int wk, bool w_early) {
+  __shared__ float part[kWarps][16][9];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+  const int kw = warp % wk, mw = warp / wk;  // this warp's share of the inputs, and its 16 outputs
+  const int per = blockDim.x / 32 / wk;      // output tiles of the CTA
+  const int64_t tile0 = (int64_t)blockIdx.x * per;
+  const int b = blockIdx.y;
+  const CodeRows cr(w, b, (tile0 + mw) * 16 + g, t);
+  const __nv_bfloat16* p = X + (int64_t)g * w.s.nblocks * w.s.cols + (int64_t)b * w.s.cols + t * 32;
+
+  float acc[4] = {};
+  Codes c[kAhead];
+  // weights that no kernel of this stream is still writing may be asked for ahead of the wait
+  if (!w_early) ptx::griddep_wait();
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) c[i] = cr.at(kw + i * wk);
+  if (w_early) ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+
+  for (int ka0 = kw; ka0 < cr.katoms; ka0 += kAhead * wk) {
+    if (ka0 != kw) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) c[i] = cr.at(ka0 + i * wk);
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int ka = ka0 + i * wk;
+      if (ka >= cr.katoms) break;
+      uint32_t x[4][8], a0[16], a1[16];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) load8<VEC>(p + ka * 128 + 8 * v, g < rows ? w.s.cols - ka * 128 - t * 32 - 8 * v : 0, x[v]);
+      values(c[i], t, a0, a1);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        uint32_t bp[1][4];
+        split8<1>(x[v], bp, (const __nv_bfloat16*)nullptr);
+        product<1>(acc, a0, a1, v, bp);
+      }
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) part[warp][g + 8 * (e >> 1)][2 * t + (e & 1)] = acc[e];
+  __syncthreads();
+  // join the shares in order; consecutive threads take consecutive outputs of one token
+  for (int e = threadIdx.x; e < per * 128; e += blockDim.x) {
+    const int row = e % 16, tile = (e / 16) % per, n = e / (16 * per);
+    const int64_t out = (tile0 + tile) * 16 + row;
+    if (out >= w.s.rows || n >= rows) continue;
+    float v = 0.f;
+    for (int k = 0; k < wk; ++k) v += part[tile * wk + k][row][n];
+    if (bias != nullptr) v += mx4::load(bias + (int64_t)b * w.s.rows + out);
+    st_from_f32(Y + o.at(b, n, out), v);
+  }
+}
+
+// Shared memory of mx4_batch_kernel: PARTS copies of 8 * NT tokens x kAhead scale tiles in bf16, 16-byte
+// chunks of 8 inputs (pairs j, j + 4), chunk c of token r at c ^ swizzle(c, r) so that the lanes of a
+// load find eight different bank groups; later the sums [per][8 * NT][kSumPitch].
+__device__ __forceinline__ int chunk_at(int token, int c) {
+  return token * (kAhead * 16) + (c ^ (((c >> 3) & 1) | ((token & 1) << 1)));
+}
+
+constexpr int kSumPitch = 20;  // 16 outputs of a token, padded: 16-byte reads, few bank conflicts
+
+// All 8 warps bring the inputs in; the first `per` compute.
 template <typename TX, int PARTS, typename TY, bool VEC, int NT>
-cudaError_t launch(const void* X, const Mx4View& w, const void* bias, int64_t rows, const Mx4Out& o, void* Y, bool w_early,
-                   cudaStream_t st) {
-  int wk = 1;
-  while (wk < kWarps && wk * 2 <= w.s.katoms()) wk *= 2;
-  const int64_t mtiles = (w.s.rows + 127) / 128 * 8;
-  const int per = kWarps / wk;
-  return launch_kernel(mx4_rows_kernel<TX, PARTS, TY, VEC, NT>,
-                       dim3((unsigned)((mtiles + per - 1) / per), (unsigned)w.s.nblocks, (unsigned)((rows + 8 * NT - 1) / (8 * NT))),
-                       dim3(kWarps * 32), 0, st, true, (const TX*)X, w, rows, o, (const TY*)bias, (TY*)Y, wk, w_early);
+__global__ void __launch_bounds__(kWarps * 32, PARTS > 1 && NT == 8 ? 1 : 2)  // two CTAs an SM where shared memory holds them
+    mx4_batch_kernel(const TX* X, Mx4View w, int64_t rows, Mx4Out o, const TY* bias, TY* Y, int shares, int per, bool w_early) {
+  constexpr int U = sizeof(TX) == 2 ? 8 : 4;  // chunks of 8 inputs a thread asks for before it stores the first
+  extern __shared__ uint4 xs[];  // [PARTS][8 * NT][kAhead * 16]
+  constexpr int PLANE = 8 * NT * kAhead * 16;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+  const int rank = (int)ptx::cluster_ctarank();
+  const bool works = warp < per;  // output tiles of the CTA, one a warp
+  const int64_t tile0 = (int64_t)(blockIdx.x / shares) * per;
+  const int b = blockIdx.y;
+  const int64_t r0 = (int64_t)blockIdx.z * (8 * NT);
+  const int tokens = (int)min((int64_t)(8 * NT), rows - r0);
+  const int64_t pitch = (int64_t)w.s.nblocks * w.s.cols;
+  const TX* xb = X + r0 * pitch + (int64_t)b * w.s.cols;
+  const CodeRows cr(w, b, (tile0 + warp) * 16 + g, t);
+  // this CTA's scale tiles: consecutive ones, kAhead at a time
+  const int each = (cr.katoms + shares - 1) / shares;
+  const int lo = rank * each, hi = min(cr.katoms, lo + each);
+
+  float acc[NT][4] = {};
+  Codes c[kAhead];
+  if (!w_early) ptx::griddep_wait();
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i)
+    if (works && lo + i < hi) c[i] = cr.at(lo + i);
+  if (w_early) ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+
+  for (int ka0 = lo; ka0 < hi; ka0 += kAhead) {
+    const int n = min(kAhead, hi - ka0);
+    if (ka0 != lo) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (works && i < n) c[i] = cr.at(ka0 + i);
+      __syncthreads();  // the previous inputs have been read
+    }
+    for (int e0 = threadIdx.x; e0 < tokens * n * 16; e0 += U * kWarps * 32) {
+      uint32_t x[U][8];
+      int token[U], ch[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int e = e0 + u * kWarps * 32;
+        token[u] = e / (n * 16);
+        ch[u] = e - token[u] * (n * 16);
+        load8<VEC>(xb + token[u] * pitch + ka0 * 128 + ch[u] * 8, token[u] < tokens ? w.s.cols - ka0 * 128 - ch[u] * 8 : 0, x[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        uint32_t bp[PARTS][4];
+        split8<PARTS>(x[u], bp, (const TX*)nullptr);
+        if (token[u] < tokens) {
+#pragma unroll
+          for (int q = 0; q < PARTS; ++q)
+            xs[q * PLANE + chunk_at(token[u], ch[u])] = make_uint4(bp[q][0], bp[q][1], bp[q][2], bp[q][3]);
+        }
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (i >= n || !works) break;
+      uint32_t a0[16], a1[16];
+      values(c[i], t, a0, a1);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        if (nt * 8 >= tokens) break;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          uint32_t bp[PARTS][4];
+#pragma unroll
+          for (int q = 0; q < PARTS; ++q) {
+            // columns of tokens behind the last are never stored: any finite or other value may stand there
+            const uint4 u = xs[q * PLANE + chunk_at(nt * 8 + g, i * 16 + t * 4 + v)];
+            bp[q][0] = u.x; bp[q][1] = u.y; bp[q][2] = u.z; bp[q][3] = u.w;
+          }
+          product<PARTS>(acc[nt], a0, a1, v, bp);
+        }
+      }
+    }
+  }
+  __syncthreads();
+  float* part = (float*)xs;
+  if (works) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        part[(warp * 8 * NT + nt * 8 + 2 * t + (e & 1)) * kSumPitch + g + 8 * (e >> 1)] = acc[nt][e];
+  }
+  ptx::cluster_sync_all();
+  // join the shares in order; four neighbouring outputs of one token a thread, consecutive threads take
+  // consecutive outputs, the cluster's CTAs take turns
+  for (int e = rank * kWarps * 32 + threadIdx.x; e < per * 4 * tokens; e += shares * kWarps * 32) {
+    const int q = e % 4, tile = (e / 4) % per, n = e / (4 * per);
+    const int64_t out = (tile0 + tile) * 16 + q * 4;
+    if (out >= w.s.rows) continue;
+    const uint32_t at = ptx::smem_u32(&part[(tile * 8 * NT + n) * kSumPitch + q * 4]);
+    float4 u[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < shares) u[k] = ptx::ld_cluster_f32x4(ptx::mapa_shared(at, k));
+    float v[4] = {};
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < shares) {
+        v[0] += u[k].x;
+        v[1] += u[k].y;
+        v[2] += u[k].z;
+        v[3] += u[k].w;
+      }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (out + i >= w.s.rows) break;
+      if (bias != nullptr) v[i] += mx4::load(bias + (int64_t)b * w.s.rows + out + i);
+      st_from_f32(Y + o.at(b, r0 + n, out + i), v[i]);
+    }
+  }
+  ptx::cluster_sync_all();  // the others may still read this CTA's sums
+}
+
+int shares_for(const Mx4View& w) {
+  int shares = 1;
+  while (shares < 8 && shares * 2 <= w.s.katoms()) shares *= 2;
+  return shares;
+}
+
+template <typename TY, bool VEC>
+cudaError_t launch_token(const void* X, const Mx4View& w, const void* bias, int64_t rows, const Mx4Out& o, void* Y, bool w_early,
+                         cudaStream_t st) {
+  const int wk = shares_for(w);
+  const int64_t mtiles = (w.s.rows + 15) / 16;
+  const int per = (int)(mtiles < kWarps / wk ? mtiles : kWarps / wk);
+  return launch_kernel(mx4_token_kernel<TY, VEC>, dim3((unsigned)((mtiles + per - 1) / per), (unsigned)w.s.nblocks),
+                       dim3(wk * per * 32), 0, st, true, (const __nv_bfloat16*)X, w, rows, o, (const TY*)bias, (TY*)Y, wk, w_early);
+}
+
+template <typename TX, int PARTS, typename TY, bool VEC, int NT>
+cudaError_t launch_batch(const void* X, const Mx4View& w, const void* bias, int64_t rows, const Mx4Out& o, void* Y, bool w_early,
+                         cudaStream_t st) {
+  const int shares = shares_for(w);
+  const int64_t mtiles = (w.s.rows + 15) / 16;
+  const int per = (int)(mtiles < kWarps ? mtiles : kWarps);
+  const size_t inputs = (size_t)PARTS * 8 * NT * kAhead * 256, sums = (size_t)per * 8 * NT * kSumPitch * 4;
+  const size_t smem = inputs > sums ? inputs : sums;
+  cudaError_t e = ensure_smem_attr((const void*)mx4_batch_kernel<TX, PARTS, TY, VEC, NT>, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((mtiles + per - 1) / per * shares), (unsigned)w.s.nblocks, (unsigned)((rows + 8 * NT - 1) / (8 * NT)));
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {(unsigned)shares, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, mx4_batch_kernel<TX, PARTS, TY, VEC, NT>, (const TX*)X, w, rows, o, (const TY*)bias, (TY*)Y, shares, per,
+                         w_early);
+  if (e == cudaSuccess) launch_counter().fetch_add(1, std::memory_order_relaxed);
+  return e;
+}
+
+template <typename TX, int PARTS, typename TY, bool VEC>
+cudaError_t launch_vec(const void* X, const Mx4View& w, const void* bias, int64_t rows, const Mx4Out& o, void* Y, bool w_early,
+                       cudaStream_t st) {
+  if (rows <= 8) {
+    if constexpr (PARTS == 1)
+      return launch_token<TY, VEC>(X, w, bias, rows, o, Y, w_early, st);
+    else
+      return launch_batch<TX, PARTS, TY, VEC, 1>(X, w, bias, rows, o, Y, w_early, st);
+  }
+  return rows <= 16   ? launch_batch<TX, PARTS, TY, VEC, 2>(X, w, bias, rows, o, Y, w_early, st)
+         : rows <= 32 ? launch_batch<TX, PARTS, TY, VEC, 4>(X, w, bias, rows, o, Y, w_early, st)
+                      : launch_batch<TX, PARTS, TY, VEC, 8>(X, w, bias, rows, o, Y, w_early, st);
 }
 
 template <typename TX, int PARTS, typename TY>
 cudaError_t launch_rows(const void* X, const Mx4View& w, const void* bias, int64_t rows, const Mx4Out& o, void* Y, bool w_early,
                         cudaStream_t st) {
-  const bool vec = w.s.cols * sizeof(TX) % 16 == 0;
-  if (rows <= 8)
-    return vec ? launch<TX, PARTS, TY, true, 1>(X, w, bias, rows, o, Y, w_early, st)
-               : launch<TX, PARTS, TY, false, 1>(X, w, bias, rows, o, Y, w_early, st);
-  if (rows <= 16)
-    return vec ? launch<TX, PARTS, TY, true, 2>(X, w, bias, rows, o, Y, w_early, st)
-               : launch<TX, PARTS, TY, false, 2>(X, w, bias, rows, o, Y, w_early, st);
-  return vec ? launch<TX, PARTS, TY, true, 4>(X, w, bias, rows, o, Y, w_early, st)
-             : launch<TX, PARTS, TY, false, 4>(X, w, bias, rows, o, Y, w_early, st);
+  return w.s.cols * sizeof(TX) % 16 == 0 ? launch_vec<TX, PARTS, TY, true>(X, w, bias, rows, o, Y, w_early, st)
+                                         : launch_vec<TX, PARTS, TY, false>(X, w, bias, rows, o, Y, w_early, st);
 }
 
 }  // namespace
