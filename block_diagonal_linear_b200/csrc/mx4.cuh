@@ -74,12 +74,6 @@ __device__ __forceinline__ uint32_t encode8(const float (&v)[8]) {
       : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
   return r;
 }
-// Value of one code without its scale.
-__device__ __forceinline__ float decode(uint32_t code) {
-  const uint32_t m = code & 7u;
-  const float a = m < 2 ? 0.5f * (float)m : __uint_as_float(((126u + (m >> 1)) << 23) | ((m & 1u) << 22));
-  return (code & 8u) ? -a : a;
-}
 // Eight codes to bf16 without their scale, divided by 2^126: the E2M1 exponent and mantissa bits land
 // on the bf16 ones, so that one multiplication by a power of two finishes the job (a code of 0.5 is a
 // bf16 subnormal here and becomes a normal number by it).  p[j] holds codes j (low half) and j + 4.
@@ -90,6 +84,24 @@ __device__ __forceinline__ void spread8(uint32_t w, uint32_t (&p)[4]) {
   p[3] = (w & 0x80008000u) | ((w >> 6) & 0x01c001c0u);
 }
 
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// Eight codes and their scale byte to bf16 pairs (2i, 2i + 1); every product is exact, subnormals and all.
+__device__ __forceinline__ void values8(uint32_t w, uint32_t byte, uint32_t (&v)[4]) {
+  const uint32_t s = (byte == 0 ? 0x0040u : byte == 255 ? 0x7fc0u : byte << 7) * 0x00010001u;  // 2^(byte - 127)
+  uint32_t p[4];
+  spread8(w, p);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) p[j] = mul_bf16x2(mul_bf16x2(p[j], 0x7e807e80u), s);  // 2^126 first
+  v[0] = __byte_perm(p[0], p[1], 0x5410);
+  v[1] = __byte_perm(p[2], p[3], 0x5410);
+  v[2] = __byte_perm(p[0], p[1], 0x7632);
+  v[3] = __byte_perm(p[2], p[3], 0x7632);
+}
+
 }  // namespace mx4
 
 // ---- launchers (cudaError_t; arguments already checked) ----
@@ -97,6 +109,8 @@ __device__ __forceinline__ void spread8(uint32_t w, uint32_t (&p)[4]) {
 cudaError_t mx4_quantise(const void* X, const Mx4Shape& s, bool by_block, int dtype, uint8_t* codes, uint8_t* scales,
                          cudaStream_t st);
 cudaError_t mx4_dequantise(const Mx4View& q, bool by_block, int dtype, void* X, cudaStream_t st);
+// The values in bf16 as (nblocks, rows, pitch), zeros behind cols; pitch a multiple of 16, out 32-byte aligned.
+cudaError_t mx4_expand(const Mx4View& q, void* out, int pitch, cudaStream_t st);
 
 // Where result (block b, row m, column n) of a product goes.
 struct Mx4Out {

@@ -351,32 +351,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- operand preparation
-// out[b][r][c] = value of element (b, r, c), zero for cols <= c < pitch (a multiple of 8).  One thread
-// turns 8 codes into 16 bytes; bound by the write of 2 bytes a value.
-__global__ void __launch_bounds__(256) mx4_expand_kernel(Mx4View q, __nv_bfloat16* __restrict__ out, int pitch) {
-  ptx::griddep_wait();
-  ptx::griddep_launch_dependents();
-  const int words = pitch / 8;
-  const int64_t total = (int64_t)q.s.nblocks * q.s.rows * words;
-  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += (int64_t)gridDim.x * 256) {
-    const int64_t row = e / words;
-    const int c = (int)(e - row * words);
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (c * 8 < q.s.kblocks() * 32) {
-      const int b = (int)(row / q.s.rows);
-      const int64_t r = row - (int64_t)b * q.s.rows;
-      const uint32_t w = *(const uint32_t*)(q.codes + row * q.s.pitch() + c * 4);
-      const float f = mx4::scale_value(q.scales[q.s.scale_at(b, r, c >> 2)]);
-      float x[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = mx4::decode((w >> (4 * i)) & 15u) * f;
-      v = make_uint4(ptx::pack_bf16x2(x[0], x[1]), ptx::pack_bf16x2(x[2], x[3]), ptx::pack_bf16x2(x[4], x[5]),
-                     ptx::pack_bf16x2(x[6], x[7]));
-    }
-    *(uint4*)(out + row * pitch + c * 8) = v;
-  }
-}
-
 // out[r][b][p][c] = part p of X[r][b*cols + c], zero behind cols; PARTS = 1 copies bf16, PARTS = 3 cuts
 // fp32 into three bf16 parts, the smallest first (see above; infinities and NaN stay in the largest).
 template <typename T, int PARTS>
@@ -612,11 +586,7 @@ size_t dw_part_bytes(const Mx4Linear& d) {
   return p.nsplit > 1 ? al256((size_t)p.nsplit * d.nb * d.out * d.in * 4) : 0;
 }
 
-cudaError_t expand(const Mx4View& q, void* out, cudaStream_t st) {
-  const int pitch = up(q.s.cols, 64);
-  return launch_kernel(mx4_expand_kernel, dim3(blocks_for((int64_t)q.s.nblocks * q.s.rows * (pitch / 8))), dim3(256), 0, st, true,
-                       q, (__nv_bfloat16*)out, pitch);
-}
+cudaError_t expand(const Mx4View& q, void* out, cudaStream_t st) { return mx4_expand(q, out, up(q.s.cols, 64), st); }
 // The K-major view of a plain operand (staged into `ws` if needed).
 cudaError_t stage(const void* X, const Mx4Linear& d, int blk, void* ws, Operand* o, cudaStream_t st) {
   const int parts = parts_of(d.dtype);
