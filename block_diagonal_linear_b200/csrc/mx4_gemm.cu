@@ -209,12 +209,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         int lo, hi;
         stage_range(job, c.split, &lo, &hi);
         const int slot = n & 1;
-        if (!warp_wait_or_abort(lane, &bars->acc_empty[slot], ((n >> 1) & 1) ^ 1, abort_flag, status)) { ok = false; break; }
+        if (!all_wait_or_abort(&bars->acc_empty[slot], ((n >> 1) & 1) ^ 1, abort_flag, status)) { ok = false; break; }
         ptx::tc_fence_after();
         const uint32_t d = tmem + slot * C::BN;
         for (int kb = lo; kb < hi; ++kb, ++it) {
           const int st = it % C::NSTAGE;
-          if (!warp_wait_or_abort(lane, &bars->full[st], (it / C::NSTAGE) & 1, abort_flag, status)) { ok = false; break; }
+          if (!all_wait_or_abort(&bars->full[st], (it / C::NSTAGE) & 1, abort_flag, status)) { ok = false; break; }
           ptx::tc_fence_after();
           const uint64_t soff = (uint64_t)((st * C::STAGE) >> 4);
 #pragma unroll
