@@ -23,7 +23,7 @@
 // epilogue: two warps a TMEM lane quadrant, one row a thread, alternate 128-byte chunks of columns.  Each
 // warp stages and stores its own 32 rows, so that no warp waits for another (with four warps that met at
 // barriers around a common staging buffer the epilogue bounded short K: 10000 rows of four 256 -> 1024
-// blocks took 28.4 us, now @F@).
+// blocks took 28.4 us, now 20.4).
 #include "mx4.cuh"
 #include "tc_common.cuh"
 
@@ -34,7 +34,7 @@ namespace {
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr uint32_t kSfCol = 472;  // first TMEM column of the scales
-constexpr int kSlab = 32 * 128;  // a warp's 32 rows x 128 bytes; two of them a warp
+constexpr int kSlab = 32 * 128;  // a warp's 32 rows x 128 bytes of output
 
 struct Job {
   int nb, mtiles, ntiles;
@@ -55,8 +55,11 @@ struct Cfg {
   static constexpr int SFA_BYTES = 1024, SFB_BYTES = 1024 * NT;
   static constexpr int STAGE = A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES;
   static constexpr int SLOT1 = BN == 256 ? 216 : BN;     // first column of the second accumulator
-  static constexpr int STG_BYTES = 2 * kEpiWarps * kSlab;
-  static constexpr int TAIL = 4096;
+  // output slabs of a warp; a pair's long products want a fifth stage more than a second slab (8192 x 4096 -> 4096:
+  // 63.6 us with two, 60.6 with one), short ones the slab
+  static constexpr int SLABS = PAIR ? 1 : 2;
+  static constexpr int STG_BYTES = SLABS * kEpiWarps * kSlab;
+  static constexpr int TAIL = 5120;
   static constexpr int NSTAGE_RAW = (kSmemBudget - STG_BYTES - TAIL) / STAGE;
   static constexpr int NSTAGE = NSTAGE_RAW > 8 ? 8 : NSTAGE_RAW;
   static constexpr int SMEM_BYTES = STG_BYTES + NSTAGE * STAGE + TAIL + 1024;
@@ -70,9 +73,9 @@ struct Bars {
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort_flag;
-  alignas(16) float bias[kEpiWarps][64];
+  alignas(16) float bias[kEpiWarps][128];  // of a warp's chunks of the current tile
 };
-static_assert(sizeof(Bars) <= 4096, "bars");
+static_assert(sizeof(Bars) <= 5120, "bars");
 
 // Instruction descriptor of kind::mxf4: A, B E2M1, scales E8M0, byte pair `pair` of the scale words.
 __host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N, int pair) {
@@ -87,12 +90,13 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
 struct Unit {
   int b, mt, nt;
 };
-__device__ __forceinline__ Unit unit_at(const Job& j, int64_t u) {
+__device__ __forceinline__ Unit unit_at(const Job& j, int64_t unit) {
   Unit c;
-  c.nt = (int)(u % j.ntiles);
-  u /= j.ntiles;
-  c.b = (int)(u % j.nb);
-  c.mt = (int)(u / j.nb);
+  uint32_t u = (uint32_t)unit;  // Y would be larger than any memory before this overflows; checked on the host
+  c.nt = (int)(u % (uint32_t)j.ntiles);
+  u /= (uint32_t)j.ntiles;
+  c.b = (int)(u % (uint32_t)j.nb);
+  c.mt = (int)(u / (uint32_t)j.nb);
   return c;
 }
 
@@ -265,21 +269,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int NCH = C::BN / CC;
     const int ew = warp - 2, quad = warp & 3, half = ew >> 2;  // warps 2..5: even chunks, 6..9: odd ones
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-    uint8_t* slab = stg + ew * 2 * kSlab;
+    uint8_t* slab = stg + ew * C::SLABS * kSlab;
     const uint32_t slab_s = ptx::smem_u32(slab);
     float* bias_s = bars->bias[ew];
     const uint32_t next0 = PAIR ? ptx::mapa_shared(ptx::smem_u32(&bars->acc_next), 0) : 0u;
     const int64_t pitch = (int64_t)job.nb * job.out;
+    constexpr int MINE = (NCH + 1) / 2;  // chunks of a warp
+    constexpr int NB = MINE * CC / 32;
+    float next_bias[NB];
+    auto fetch_bias = [&](int64_t u) {
+      const Unit c = unit_at(job, u);
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        const int ch = (32 * i / CC) * 2 + half, col = c.nt * C::BN + ch * CC + (32 * i) % CC + lane;
+        next_bias[i] = u < job.units && ch < NCH && col < job.out ? mx4::load(bias + (int64_t)c.b * job.out + col) : 0.f;
+      }
+    };
+    if (bias != nullptr) fetch_bias(cl);
     uint32_t n = 0, stored = 0;
     for (int64_t u = cl; u < job.units; u += ncl, ++n) {
       const Unit c = unit_at(job, u);
       const int slot = n & 1;
       const int n0 = c.nt * C::BN;
       const int64_t m0 = (int64_t)c.mt * C::BM + (int64_t)rank * 128 + quad * 32;  // this warp's rows
+      if (bias != nullptr) {
+        __syncwarp();  // the previous tile's has been read
+#pragma unroll
+        for (int i = 0; i < NB; ++i) bias_s[32 * i + lane] = next_bias[i];
+        __syncwarp();
+        fetch_bias(u + ncl);  // asked for a tile ahead: the epilogue has no time to wait for it
+      }
       if (!all_wait_or_abort(&bars->acc_full[slot], (n >> 1) & 1, abort_flag, status)) break;
       ptx::tc_fence_after();
       const uint32_t tb = tmem + lane_off + slot * C::SLOT1;
-      constexpr int MINE = (NCH + 1) / 2;  // chunks of a warp
 #pragma unroll 1
       for (int i = 0; i < MINE; ++i) {
         // the first accumulator's shared columns are its last
@@ -308,21 +330,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!live) continue;
         if (bias != nullptr) {
-#pragma unroll
-          for (int e = lane; e < CC; e += 32)
-            bias_s[e] = n0 + ch * CC + e < job.out ? mx4::load(bias + (int64_t)c.b * job.out + n0 + ch * CC + e) : 0.f;
-          __syncwarp();
+          const float* bs = bias_s + (ch >> 1) * CC;
 #pragma unroll
           for (int e = 0; e < CC; e += 4) {
-            const float4 f = *(const float4*)(bias_s + e);
+            const float4 f = *(const float4*)(bs + e);
             v[e] = __float_as_uint(__uint_as_float(v[e]) + f.x);
             v[e + 1] = __float_as_uint(__uint_as_float(v[e + 1]) + f.y);
             v[e + 2] = __float_as_uint(__uint_as_float(v[e + 2]) + f.z);
             v[e + 3] = __float_as_uint(__uint_as_float(v[e + 3]) + f.w);
           }
         }
-        const int sbuf = stored++ & 1;
-        if (TMA_OUT && lane == 0) ptx::bulk_wait_read_allbut1();  // what last left this slab has been read
+        const int sbuf = stored++ % C::SLABS;
+        if (TMA_OUT && lane == 0) {  // what last left this slab has been read
+          if (C::SLABS == 2)
+            ptx::bulk_wait_read_allbut1();
+          else
+            ptx::bulk_wait_read_all();
+        }
         __syncwarp();
         const uint32_t base = slab_s + sbuf * kSlab + lane * 128;
 #pragma unroll
@@ -419,6 +443,7 @@ cudaError_t launch(const Mx4View& x, const Mx4View& w, const void* bias, const M
   j.mtiles = (int)((d.rows + C::BM - 1) / C::BM);
   j.ntiles = (d.out + C::BN - 1) / C::BN;
   j.units = (int64_t)j.nb * j.mtiles * j.ntiles;
+  if (j.units > (int64_t(1) << 31)) return cudaErrorInvalidValue;
   j.rows = d.rows;
   j.out = d.out;
   j.ksteps = (x.s.kblocks() + 1) / 2;
@@ -454,7 +479,10 @@ cudaError_t launch_out(const Mx4View& x, const Mx4View& w, const void* bias, con
 template <typename T>
 cudaError_t launch_type(const Mx4View& x, const Mx4View& w, const void* bias, const Mx4Linear& d, void* Y, int* status,
                         cudaStream_t st) {
-  if (d.out > 128 && (d.rows + 255) / 256 * d.nb * ((d.out + 255) / 256) >= num_sms() / 2)
+  // a pair's two CTAs wait for each other once a tile, which only a long K hides: 8192 rows -> 4096 take
+  // 19.7 us on pairs and 14.1 on single CTAs with 256 inputs, 22.2 and 17.7 with 512, 27.1 and 26.6 with 1024,
+  // 60.6 and 75 with 4096
+  if (d.in >= 1024 && d.out > 128 && (d.rows + 255) / 256 * d.nb * ((d.out + 255) / 256) >= num_sms() / 2)
     return launch_out<256, true, T>(x, w, bias, d, Y, status, st);
   // the widest tile that the outputs fill, halved while there are fewer tiles than SMs
   int bn = d.out > 128 ? 256 : d.out > 64 ? 128 : 64;
