@@ -74,11 +74,7 @@ int status_of(cudaError_t e) { return e == cudaSuccess ? MONARCH_OK : MONARCH_ER
 constexpr int64_t kFewRows = 64;
 
 size_t wfwd_workspace(const Mx4Linear& d) { return d.rows <= kFewRows ? 0 : mx4_gemm_fwd_bytes(d); }
-// Backward: the two products' scratch, then the bias gradient's.
-size_t bwd_workspace(const Mx4Linear& d) {
-  if (d.rows == 0) return 0;
-  return mx4_gemm_bwd_bytes(d) + (d.has_bias ? al256(mx4_dbias_bytes(d.rows, (int64_t)d.nb * d.out)) : 0);
-}
+size_t bwd_workspace(const Mx4Linear& d) { return d.rows == 0 ? 0 : mx4_gemm_bwd_bytes(d); }
 
 Mx4Shape r_shape(const monarch_dims& d) { return Mx4Shape{d.out1, d.nb1, d.in1}; }
 Mx4Shape l_shape(const monarch_dims& d) { return Mx4Shape{d.out2, d.nb2, d.in2}; }
@@ -223,10 +219,7 @@ int monarch_mx4_linear_bwd(const void* dY, const void* x_codes, const void* x_sc
   }
   int* status = status_ptr();
   if (status == nullptr) return MONARCH_ERR_CUDA;
-  if ((dX != nullptr || dW != nullptr) && mx4_gemm_bwd(dY, x, w, d, dX, dW, workspace, status, st) != cudaSuccess)
-    return MONARCH_ERR_CUDA;
-  float* part = (float*)((char*)workspace + mx4_gemm_bwd_bytes(d));
-  return d.has_bias ? status_of(mx4_dbias(dY, d.rows, n_out, d.dtype, part, dbias, st)) : MONARCH_OK;
+  return status_of(mx4_gemm_bwd(dY, x, w, d, dX, dW, d.has_bias ? dbias : nullptr, workspace, status, st));
 }
 
 size_t monarch_mx4_fwd_workspace_bytes(const monarch_dims* d) {

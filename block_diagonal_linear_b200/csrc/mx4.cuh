@@ -109,8 +109,6 @@ __device__ __forceinline__ void values8(uint32_t w, uint32_t byte, uint32_t (&v)
 cudaError_t mx4_quantise(const void* X, const Mx4Shape& s, bool by_block, int dtype, uint8_t* codes, uint8_t* scales,
                          cudaStream_t st);
 cudaError_t mx4_dequantise(const Mx4View& q, bool by_block, int dtype, void* X, cudaStream_t st);
-// The values in bf16 as (nblocks, rows, pitch), zeros behind cols; pitch a multiple of 16, out 32-byte aligned.
-cudaError_t mx4_expand(const Mx4View& q, void* out, int pitch, cudaStream_t st);
 
 // Where result (block b, row m, column n) of a product goes.
 struct Mx4Out {
@@ -138,16 +136,12 @@ cudaError_t mx4_tc_fwd(const Mx4View& x, const Mx4View& w, const void* bias, con
 cudaError_t mx4_rows_fwd(const void* X, int x_dtype, const Mx4View& w, const void* bias, int64_t rows, const Mx4Out& o, void* Y,
                          int y_dtype, bool w_early, cudaStream_t st);
 // Products with a plain operand on the bf16 tensor cores, every size and both types (mx4_gemm.cu); ws: the
-// bytes that the size query gives.  dX or dW may be NULL.
+// bytes that the size query gives.  dX, dW and dbias may be NULL.
 size_t mx4_gemm_fwd_bytes(const Mx4Linear& d);
 cudaError_t mx4_gemm_fwd(const void* X, const Mx4View& w, const void* bias, const Mx4Linear& d, void* Y, void* ws, int* status,
                          cudaStream_t st);
 size_t mx4_gemm_bwd_bytes(const Mx4Linear& d);
-cudaError_t mx4_gemm_bwd(const void* dY, const Mx4View& x, const Mx4View& w, const Mx4Linear& d, void* dX, void* dW, void* ws,
-                         int* status, cudaStream_t st);
-// dbias[c] = sum over rows of dY[r][c], rows in a fixed order; part: mx4_dbias_bytes of scratch.
-size_t mx4_dbias_bytes(int64_t rows, int64_t cols);
-cudaError_t mx4_dbias(const void* dY, int64_t rows, int64_t cols, int dtype, float* part, void* dbias,
-                      cudaStream_t st);
+cudaError_t mx4_gemm_bwd(const void* dY, const Mx4View& x, const Mx4View& w, const Mx4Linear& d, void* dX, void* dW, void* dbias,
+                         void* ws, int* status, cudaStream_t st);
 
 }  // namespace monarch

@@ -70,14 +70,15 @@ struct GUnit {
   int b, mt, nt, split;
 };
 // n tile fastest, then block, m tile, split
-__device__ __forceinline__ GUnit unit_at(const GJob& j, int64_t u) {
+__device__ __forceinline__ GUnit unit_at(const GJob& j, int64_t unit) {
   GUnit c;
-  c.nt = (int)(u % j.ntiles);
-  u /= j.ntiles;
-  c.b = (int)(u % j.nb);
-  u /= j.nb;
-  c.mt = (int)(u % j.mtiles);
-  c.split = (int)(u / j.mtiles);
+  uint32_t u = (uint32_t)unit;  // checked on the host
+  c.nt = (int)(u % (uint32_t)j.ntiles);
+  u /= (uint32_t)j.ntiles;
+  c.b = (int)(u % (uint32_t)j.nb);
+  u /= (uint32_t)j.nb;
+  c.mt = (int)(u % (uint32_t)j.mtiles);
+  c.split = (int)(u / (uint32_t)j.mtiles);
   return c;
 }
 __device__ __forceinline__ void stage_range(const GJob& j, int split, int* lo, int* hi) {
@@ -351,90 +352,200 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- operand preparation
-// out[r][b][p][c] = part p of X[r][b*cols + c], zero behind cols; PARTS = 1 copies bf16, PARTS = 3 cuts
-// fp32 into three bf16 parts, the smallest first (see above; infinities and NaN stay in the largest).
-template <typename T, int PARTS>
-__global__ void __launch_bounds__(256) mx4_stage_kernel(const T* __restrict__ X, int64_t nrb, int cols,
-                                                        __nv_bfloat16* __restrict__ out, int pitch) {
-  ptx::griddep_wait();
-  ptx::griddep_launch_dependents();
-  const int words = pitch / 2;
-  const int64_t total = nrb * words;
-  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += (int64_t)gridDim.x * 256) {
-    const int64_t row = e / words;  // (r, b)
-    const int c = (int)(e - row * words) * 2;
-    float x[2];
+// What the products need first, in one launch of up to four jobs: MX4 operands in bf16, a plain operand in
+// rows that TMA can address, and the bias gradient's partial sums (which read dY, so that the products
+// find it in L2).  A job takes a range of the blocks.
+
+// out[b][r][c] = value of element (b, r, c), zero for cols <= c < pitch (a multiple of 64): one thread a scale
+// block, 64 rows x 128 columns a CTA; bound by the write of 2 bytes a value.
+struct ExpandJob {
+  Mx4View q;
+  __nv_bfloat16* out;
+  int pitch, ktiles;
+  int64_t rtiles, blocks;  // 0 blocks: no job
+};
+__device__ __forceinline__ void expand_tile(const ExpandJob& j, int64_t blk) {
+  const Mx4Shape& s = j.q.s;
+  const int kt = (int)(blk % j.ktiles);
+  blk /= j.ktiles;
+  const int b = (int)(blk / j.rtiles);
+  const int64_t r = (blk - b * j.rtiles) * 64 + (threadIdx.x >> 2);
+  const int kb = kt * 4 + (threadIdx.x & 3);
+  if (r >= s.rows || kb * 32 >= j.pitch) return;
+  uint4 u = make_uint4(0, 0, 0, 0);
+  uint32_t byte = 0;
+  if (kb < s.kblocks()) {
+    u = *(const uint4*)(j.q.codes + s.code_row(b, r) + kb * 16);
+    byte = j.q.scales[s.scale_at(b, r, kb)];
+  }
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  uint32_t v[16];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) x[i] = c + i < cols ? mx4::load(X + row * cols + c + i) : 0.f;
-    uint32_t* dst = (uint32_t*)(out + row * PARTS * pitch + c);
+  for (int i = 0; i < 4; ++i) {
+    uint32_t t[4];
+    mx4::values8(w[i], byte, t);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[4 * i + e] = t[e];
+  }
+  __nv_bfloat16* p = j.out + ((int64_t)b * s.rows + r) * j.pitch + kb * 32;
+  ptx::st_global_v8(p, v);
+  ptx::st_global_v8(p + 16, v + 8);
+}
+
+// out[r][b][p][c] = part p of X[r][b*cols + c], zero behind cols: bf16 is copied, fp32 cut into three bf16
+// parts, the smallest first (see above; infinities and NaN stay in the largest).
+struct StageJob {
+  const void* X;
+  __nv_bfloat16* out;
+  int64_t nrb;  // rows * blocks
+  int cols, pitch;
+  int64_t blocks;
+};
+constexpr int kStagePer = 8;  // pairs of values a thread
+template <typename T>
+__device__ __forceinline__ void stage_pairs(const StageJob& j, int64_t blk) {
+  constexpr int PARTS = sizeof(T) == 2 ? 1 : 3;
+  const uint32_t words = j.pitch / 2;
+  const int64_t first = blk * (256 * kStagePer), total = j.nrb * words;
+  const T* X = (const T*)j.X;
+  float x[kStagePer][2];
+  int64_t row[kStagePer];
+  int c[kStagePer];
+#pragma unroll
+  for (int u = 0; u < kStagePer; ++u) {
+    const int64_t e = first + u * 256 + threadIdx.x;
+    row[u] = e / words;
+    c[u] = (int)(e - row[u] * words) * 2;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) x[u][i] = e < total && c[u] + i < j.cols ? mx4::load(X + row[u] * j.cols + c[u] + i) : 0.f;
+  }
+#pragma unroll
+  for (int u = 0; u < kStagePer; ++u) {
+    if (first + u * 256 + threadIdx.x >= total) break;
+    uint32_t* dst = (uint32_t*)(j.out + row[u] * PARTS * j.pitch + c[u]);
 #pragma unroll
     for (int p = PARTS - 1; p >= 0; --p) {
-      dst[p * words] = (__float_as_uint(x[0]) >> 16) | (__float_as_uint(x[1]) & 0xffff0000u);
+      dst[p * words] = (__float_as_uint(x[u][0]) >> 16) | (__float_as_uint(x[u][1]) & 0xffff0000u);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const uint32_t top = __float_as_uint(x[i]) & 0xffff0000u;
-        x[i] = (top & 0x7f800000u) == 0x7f800000u ? 0.f : x[i] - __uint_as_float(top);
+        const uint32_t top = __float_as_uint(x[u][i]) & 0xffff0000u;
+        x[u][i] = (top & 0x7f800000u) == 0x7f800000u ? 0.f : x[u][i] - __uint_as_float(top);
       }
     }
   }
 }
 
-// out[e] = sum over s of part[s][e], in order.
-template <typename T>
-__global__ void __launch_bounds__(256) mx4_sum_kernel(const float* __restrict__ part, int64_t n, int nsplit, T* __restrict__ out) {
-  ptx::griddep_wait();
-  ptx::griddep_launch_dependents();
-  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < n; e += (int64_t)gridDim.x * 256) {
-    float acc = 0.f;
-    for (int s = 0; s < nsplit; ++s) acc += part[(int64_t)s * n + e];
-    st_from_f32(out + e, acc);
+// part[k][c] = sum of rows [k * kBiasRows, + kBiasRows) of dY's column c, in a fixed order: a warp takes
+// every eighth row, a lane 16 bytes of it (or one element where rows are no multiple of 16 bytes).  With one
+// part the sums are dbias.
+constexpr int kBiasRows = 256;
+struct BiasJob {
+  const void* dY;
+  float* part;
+  void* dbias;
+  int64_t rows, cols;
+  int cgroups;
+  int64_t nparts, blocks;
+};
+template <typename T, bool VEC>
+__device__ __forceinline__ void bias_part(const BiasJob& j, int64_t blk, float (*sums)[32 * 8]) {
+  constexpr int W = VEC ? 16 / sizeof(T) : 1;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int64_t k = blk / j.cgroups;
+  const int64_t c0 = (blk - k * j.cgroups) * (32 * W), c = c0 + lane * W;
+  const int64_t r0 = k * kBiasRows, r1 = min(j.rows, r0 + kBiasRows);
+  const T* p = (const T*)j.dY + c;
+  float acc[W] = {};
+  if (c < j.cols) {
+    constexpr int U = 8;  // rows in flight
+    for (int64_t r = r0 + warp; r < r1; r += 8 * U) {
+      if (VEC) {
+        uint4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] = r + 8 * u < r1 ? *(const uint4*)(p + (r + 8 * u) * j.cols) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (sizeof(T) == 2) {
+              acc[(2 * i) % W] += __uint_as_float(w[i] << 16);
+              acc[(2 * i + 1) % W] += __uint_as_float(w[i] & 0xffff0000u);
+            } else {
+              acc[i % W] += __uint_as_float(w[i]);
+            }
+          }
+        }
+      } else {
+        float v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] = r + 8 * u < r1 ? mx4::load(p + (r + 8 * u) * j.cols) : 0.f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) acc[0] += v[u];
+      }
+    }
   }
-}
-
-// ---------------------------------------------------------------- bias gradient
-// Column sums of dY in two steps: every CTA sums kBiasRows rows of 64 columns in fp32 (four row
-// lanes, joined in a fixed order), then one thread per column adds the parts in order.
-constexpr int kBiasRows = 256, kBiasCols = 64;
-
-template <typename T>
-__global__ void __launch_bounds__(256) mx4_dbias_part_kernel(const T* __restrict__ dY, int64_t rows, int64_t cols,
-                                                             float* __restrict__ part) {
-  __shared__ float s[4][kBiasCols];
-  ptx::griddep_wait();
-  ptx::griddep_launch_dependents();
-  const int c = threadIdx.x % kBiasCols, lane = threadIdx.x / kBiasCols;
-  const int64_t col = (int64_t)blockIdx.y * kBiasCols + c;
-  const int64_t r0 = (int64_t)blockIdx.x * kBiasRows, r1 = r0 + kBiasRows < rows ? r0 + kBiasRows : rows;
-  float acc = 0.f;
-  if (col < cols)
-    for (int64_t r = r0 + lane; r < r1; r += 4) acc += mx4::load(dY + r * cols + col);
-  s[lane][c] = acc;
+#pragma unroll
+  for (int i = 0; i < W; ++i) sums[warp][lane * W + i] = acc[i];
   __syncthreads();
-  if (lane == 0 && col < cols) part[(int64_t)blockIdx.x * cols + col] = (s[0][c] + s[1][c]) + (s[2][c] + s[3][c]);
+  for (int e = threadIdx.x; e < 32 * W; e += 256) {
+    if (c0 + e >= j.cols) break;
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) v += sums[w][e];
+    if (j.nparts == 1)
+      st_from_f32((T*)j.dbias + c0 + e, v);
+    else
+      j.part[k * j.cols + c0 + e] = v;
+  }
 }
 
 template <typename T>
-__global__ void __launch_bounds__(256) mx4_dbias_sum_kernel(const float* __restrict__ part, int64_t nparts, int64_t cols,
-                                                            T* __restrict__ dbias) {
+__global__ void __launch_bounds__(256)
+    mx4_prepare_kernel(const __grid_constant__ BiasJob bias, const __grid_constant__ ExpandJob e0, const __grid_constant__ ExpandJob e1,
+                       const __grid_constant__ StageJob stage) {
+  __shared__ float sums[8][32 * 8];
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
-  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (c >= cols) return;
-  float acc = 0.f;
-  for (int64_t k = 0; k < nparts; ++k) acc += part[k * cols + c];
-  st_from_f32(dbias + c, acc);
+  int64_t blk = blockIdx.x;
+  if (blk < bias.blocks) {
+    if (bias.cols * sizeof(T) % 16 == 0)
+      bias_part<T, true>(bias, blk, sums);
+    else
+      bias_part<T, false>(bias, blk, sums);
+    return;
+  }
+  blk -= bias.blocks;
+  if (blk < stage.blocks) {
+    stage_pairs<T>(stage, blk);
+    return;
+  }
+  blk -= stage.blocks;
+  if (blk < e0.blocks)
+    expand_tile(e0, blk);
+  else
+    expand_tile(e1, blk - e0.blocks);
 }
 
+// What is left to add at the end, parts in order: out[e] over nsplit parts of n, dbias[c] over nparts of cols.
 template <typename T>
-cudaError_t dbias_t(const void* dY, int64_t rows, int64_t cols, float* part, void* dbias, cudaStream_t st) {
-  const int64_t n = (rows + kBiasRows - 1) / kBiasRows;
-  if (n > 0) {
-    const cudaError_t e = launch_kernel(mx4_dbias_part_kernel<T>, dim3((unsigned)n, (unsigned)((cols + kBiasCols - 1) / kBiasCols)),
-                                        dim3(256), 0, st, true, (const T*)dY, rows, cols, part);
-    if (e != cudaSuccess) return e;
+__global__ void __launch_bounds__(256)
+    mx4_sum_kernel(const float* __restrict__ part, int64_t n, int nsplit, T* __restrict__ out, const float* __restrict__ bpart,
+                   int64_t cols, int64_t nparts, T* __restrict__ dbias) {
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < n + cols; e += (int64_t)gridDim.x * 256) {
+    const bool b = e >= n;
+    const float* p = b ? bpart + (e - n) : part + e;
+    const int64_t step = b ? cols : n, m = b ? nparts : nsplit;
+    float acc = 0.f;
+#pragma unroll 8
+    for (int64_t s = 0; s < m; ++s) acc += p[s * step];
+    if (b)
+      st_from_f32(dbias + (e - n), acc);
+    else
+      st_from_f32(out + e, acc);
   }
-  return launch_kernel(mx4_dbias_sum_kernel<T>, dim3((unsigned)((cols + 255) / 256)), dim3(256), 0, st, true,
-                       (const float*)part, n, cols, (T*)dbias);
 }
 
 unsigned blocks_for(int64_t threads) {
@@ -529,6 +640,7 @@ cudaError_t launch(const Operand& a, const Operand& b, const Result& d, const vo
   j.mtiles = (int)((d.m + C::BM - 1) / C::BM);
   j.ntiles = (d.n + C::BN - 1) / C::BN;
   j.units = (int64_t)j.nb * j.mtiles * j.ntiles * j.nsplit;
+  if (j.units > (int64_t(1) << 31)) return cudaErrorInvalidValue;
   cudaError_t e = ensure_smem_attr((const void*)mx4_gemm_kernel<C>, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   const int64_t slots = C::PAIR ? num_sms() / 2 : num_sms();
@@ -586,25 +698,39 @@ size_t dw_part_bytes(const Mx4Linear& d) {
   return p.nsplit > 1 ? al256((size_t)p.nsplit * d.nb * d.out * d.in * 4) : 0;
 }
 
-cudaError_t expand(const Mx4View& q, void* out, cudaStream_t st) { return mx4_expand(q, out, up(q.s.cols, 64), st); }
-// The K-major view of a plain operand (staged into `ws` if needed).
-cudaError_t stage(const void* X, const Mx4Linear& d, int blk, void* ws, Operand* o, cudaStream_t st) {
-  const int parts = parts_of(d.dtype);
-  if (direct(d.dtype, blk)) {
-    *o = Operand{X, blk, d.rows, d.nb, (int64_t)d.nb * blk, blk};
-    return cudaSuccess;
-  }
-  const int pitch = up(blk, 64);
-  *o = Operand{ws, (int64_t)parts * pitch, d.rows, d.nb, (int64_t)d.nb * parts * pitch, (int64_t)parts * pitch};
-  const int64_t nrb = d.rows * d.nb;
-  const dim3 grid(blocks_for(nrb * (pitch / 2)));
-  return d.dtype == MONARCH_BF16
-             ? launch_kernel(mx4_stage_kernel<__nv_bfloat16, 1>, grid, dim3(256), 0, st, true, (const __nv_bfloat16*)X, nrb, blk,
-                             (__nv_bfloat16*)ws, pitch)
-             : launch_kernel(mx4_stage_kernel<float, 3>, grid, dim3(256), 0, st, true, (const float*)X, nrb, blk,
-                             (__nv_bfloat16*)ws, pitch);
+ExpandJob expand_job(const Mx4View& q, void* out) {
+  ExpandJob j;
+  j.q = q;
+  j.out = (__nv_bfloat16*)out;
+  j.pitch = up(q.s.cols, 64);
+  j.ktiles = (j.pitch + 127) / 128;
+  j.rtiles = (q.s.rows + 63) / 64;
+  j.blocks = j.rtiles * j.ktiles * q.s.nblocks;
+  return j;
 }
-// The same operand with its rows as K: one batch entry per (block, part).
+// The K-major view of a plain operand, and the job that stages it into `ws` if that is needed.
+Operand staged(const void* X, const Mx4Linear& d, int blk, void* ws, StageJob* job) {
+  *job = StageJob{};
+  const int parts = parts_of(d.dtype);
+  if (direct(d.dtype, blk)) return Operand{X, blk, d.rows, d.nb, (int64_t)d.nb * blk, blk};
+  const int pitch = up(blk, 64);
+  *job = StageJob{X, (__nv_bfloat16*)ws, d.rows * d.nb, blk, pitch, 0};
+  job->blocks = (job->nrb * (pitch / 2) + 256 * kStagePer - 1) / (256 * kStagePer);
+  return Operand{ws, (int64_t)parts * pitch, d.rows, d.nb, (int64_t)d.nb * parts * pitch, (int64_t)parts * pitch};
+}
+int64_t bias_parts(const Mx4Linear& d) { return (d.rows + kBiasRows - 1) / kBiasRows; }
+size_t bias_part_bytes(const Mx4Linear& d) {
+  return d.has_bias && bias_parts(d) > 1 ? al256((size_t)bias_parts(d) * d.nb * d.out * 4) : 0;
+}
+cudaError_t prepare(const Mx4Linear& d, const BiasJob& b, const ExpandJob& e0, const ExpandJob& e1, const StageJob& s, cudaStream_t st) {
+  const int64_t blocks = b.blocks + e0.blocks + e1.blocks + s.blocks;
+  if (blocks == 0) return cudaSuccess;
+  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  return d.dtype == MONARCH_BF16
+             ? launch_kernel(mx4_prepare_kernel<__nv_bfloat16>, dim3((unsigned)blocks), dim3(256), 0, st, true, b, e0, e1, s)
+             : launch_kernel(mx4_prepare_kernel<float>, dim3((unsigned)blocks), dim3(256), 0, st, true, b, e0, e1, s);
+}
+// A K-major operand with its rows as K: one batch entry per (block, part).
 Operand rows_as_k(const Operand& o, const Mx4Linear& d, int blk) {
   if (direct(d.dtype, blk)) return o;
   const int parts = parts_of(d.dtype), pitch = up(blk, 64);
@@ -615,6 +741,21 @@ Operand expanded(const void* p, const Mx4Shape& s) {
   return Operand{p, pitch, s.rows, s.nblocks, pitch, (int64_t)pitch * s.rows};
 }
 
+// Backward scratch: the operands in bf16, split sums of dW, parts of dbias.
+struct BwdWs {
+  size_t w, x, dy, part, bias, total;
+};
+BwdWs bwd_layout(const Mx4Linear& d) {
+  BwdWs l;
+  l.w = 0;
+  l.x = l.w + expanded_bytes(d.w());
+  l.dy = l.x + expanded_bytes(d.x());
+  l.part = l.dy + staged_bytes(d, d.out);
+  l.bias = l.part + dw_part_bytes(d);
+  l.total = l.bias + bias_part_bytes(d);
+  return l;
+}
+
 }  // namespace
 
 size_t mx4_gemm_fwd_bytes(const Mx4Linear& d) { return expanded_bytes(d.w()) + staged_bytes(d, d.in); }
@@ -622,63 +763,69 @@ size_t mx4_gemm_fwd_bytes(const Mx4Linear& d) { return expanded_bytes(d.w()) + s
 cudaError_t mx4_gemm_fwd(const void* X, const Mx4View& w, const void* bias, const Mx4Linear& d, void* Y, void* ws, int* status,
                          cudaStream_t st) {
   char* wd = (char*)ws;
-  Operand a;
-  cudaError_t e;
-  if ((e = expand(w, wd, st)) != cudaSuccess) return e;
-  if ((e = stage(X, d, d.in, wd + expanded_bytes(d.w()), &a, st)) != cudaSuccess) return e;
+  StageJob sj;
+  const Operand a = staged(X, d, d.in, wd + expanded_bytes(d.w()), &sj);
+  const cudaError_t e = prepare(d, BiasJob{}, expand_job(w, wd), ExpandJob{}, sj, st);
+  if (e != cudaSuccess) return e;
   const Result r{Y, d.rows, d.out, d.nb, (int64_t)d.nb * d.out, d.out};
   const Plan p = plan_for(d.rows, d.out, d.nb, (d.in + 63) / 64 * parts_of(d.dtype), false);
   return d.dtype == MONARCH_BF16 ? gemm<false, false, __nv_bfloat16>(a, expanded(wd, d.w()), r, bias, d.nb, d.in, 1, p, status, st)
                                  : gemm<false, false, float>(a, expanded(wd, d.w()), r, bias, d.nb, d.in, 3, p, status, st);
 }
 
-size_t mx4_gemm_bwd_bytes(const Mx4Linear& d) {
-  // the expanded operand: W for dX, then X for dW in the same place
-  return std::max(expanded_bytes(d.w()), expanded_bytes(d.x())) + staged_bytes(d, d.out) + dw_part_bytes(d);
-}
+size_t mx4_gemm_bwd_bytes(const Mx4Linear& d) { return bwd_layout(d).total; }
 
-cudaError_t mx4_gemm_bwd(const void* dY, const Mx4View& x, const Mx4View& w, const Mx4Linear& d, void* dX, void* dW, void* ws,
-                         int* status, cudaStream_t st) {
-  char* ex = (char*)ws;
-  char* sy = ex + std::max(expanded_bytes(d.w()), expanded_bytes(d.x()));
-  float* part = (float*)(sy + staged_bytes(d, d.out));
+cudaError_t mx4_gemm_bwd(const void* dY, const Mx4View& x, const Mx4View& w, const Mx4Linear& d, void* dX, void* dW, void* dbias,
+                         void* ws, int* status, cudaStream_t st) {
+  const BwdWs l = bwd_layout(d);
+  char* base = (char*)ws;
   const bool bf = d.dtype == MONARCH_BF16;
   const int parts = parts_of(d.dtype);
-  Operand a;
-  cudaError_t e;
-  if ((e = stage(dY, d, d.out, sy, &a, st)) != cudaSuccess) return e;
+  const int64_t n_out = (int64_t)d.nb * d.out;
+  StageJob sj;
+  const Operand a = staged(dY, d, d.out, base + l.dy, &sj);
+  if (dX == nullptr && dW == nullptr) sj.blocks = 0;
+  BiasJob bj = {};
+  if (dbias != nullptr) {
+    const int w16 = n_out * (bf ? 2 : 4) % 16 == 0 ? (bf ? 8 : 4) : 1;  // columns a lane
+    bj = BiasJob{dY, (float*)(base + l.bias), dbias, d.rows, n_out, (int)((n_out + 32 * w16 - 1) / (32 * w16)), bias_parts(d), 0};
+    bj.blocks = bj.nparts * bj.cgroups;
+  }
+  cudaError_t e = prepare(d, bj, dX != nullptr ? expand_job(w, base + l.w) : ExpandJob{}, dW != nullptr ? expand_job(x, base + l.x) : ExpandJob{},
+                          sj, st);
+  if (e != cudaSuccess) return e;
   if (dX != nullptr) {
-    if ((e = expand(w, ex, st)) != cudaSuccess) return e;
     const Result r{dX, d.rows, d.in, d.nb, (int64_t)d.nb * d.in, d.in};
     const Plan p = plan_for(d.rows, d.in, d.nb, (d.out + 63) / 64 * parts, false);
-    e = bf ? gemm<false, true, __nv_bfloat16>(a, expanded(ex, d.w()), r, nullptr, d.nb, d.out, 1, p, status, st)
-           : gemm<false, true, float>(a, expanded(ex, d.w()), r, nullptr, d.nb, d.out, 3, p, status, st);
+    e = bf ? gemm<false, true, __nv_bfloat16>(a, expanded(base + l.w, d.w()), r, nullptr, d.nb, d.out, 1, p, status, st)
+           : gemm<false, true, float>(a, expanded(base + l.w, d.w()), r, nullptr, d.nb, d.out, 3, p, status, st);
     if (e != cudaSuccess) return e;
   }
-  if (dW == nullptr) return cudaSuccess;
-  if ((e = expand(x, ex, st)) != cudaSuccess) return e;
-  const Plan p = dw_plan(d);
-  const Operand ak = rows_as_k(a, d, d.out), b = expanded(ex, d.x());
-  const int64_t n = (int64_t)d.nb * d.out * d.in;
-  if (p.nsplit > 1) {
-    const Result r{part, d.out, d.in, (int64_t)d.nb * p.nsplit, d.in, (int64_t)d.out * d.in};
-    if ((e = gemm<true, true, float>(ak, b, r, nullptr, d.nb, d.rows, parts, p, status, st)) != cudaSuccess) return e;
-    return bf ? launch_kernel(mx4_sum_kernel<__nv_bfloat16>, dim3(blocks_for(n)), dim3(256), 0, st, true, (const float*)part, n, p.nsplit,
-                              (__nv_bfloat16*)dW)
-              : launch_kernel(mx4_sum_kernel<float>, dim3(blocks_for(n)), dim3(256), 0, st, true, (const float*)part, n, p.nsplit, (float*)dW);
+  float* part = nullptr;
+  int64_t n = 0;
+  int nsplit = 0;
+  if (dW != nullptr) {
+    const Plan p = dw_plan(d);
+    const Operand ak = rows_as_k(a, d, d.out), b = expanded(base + l.x, d.x());
+    if (p.nsplit > 1) {
+      part = (float*)(base + l.part);
+      n = n_out * d.in;
+      nsplit = p.nsplit;
+      const Result r{part, d.out, d.in, (int64_t)d.nb * p.nsplit, d.in, (int64_t)d.out * d.in};
+      e = gemm<true, true, float>(ak, b, r, nullptr, d.nb, d.rows, parts, p, status, st);
+    } else {
+      const Result r{dW, d.out, d.in, d.nb, d.in, (int64_t)d.out * d.in};
+      e = bf ? gemm<true, true, __nv_bfloat16>(ak, b, r, nullptr, d.nb, d.rows, 1, p, status, st)
+             : gemm<true, true, float>(ak, b, r, nullptr, d.nb, d.rows, 3, p, status, st);
+    }
+    if (e != cudaSuccess) return e;
   }
-  const Result r{dW, d.out, d.in, d.nb, d.in, (int64_t)d.out * d.in};
-  return bf ? gemm<true, true, __nv_bfloat16>(ak, b, r, nullptr, d.nb, d.rows, 1, p, status, st)
-            : gemm<true, true, float>(ak, b, r, nullptr, d.nb, d.rows, 3, p, status, st);
-}
-
-size_t mx4_dbias_bytes(int64_t rows, int64_t cols) {
-  return (size_t)((rows + kBiasRows - 1) / kBiasRows) * (size_t)cols * 4;
-}
-cudaError_t mx4_dbias(const void* dY, int64_t rows, int64_t cols, int dtype, float* part, void* dbias,
-                      cudaStream_t st) {
-  return dtype == MONARCH_BF16 ? dbias_t<__nv_bfloat16>(dY, rows, cols, part, dbias, st)
-                               : dbias_t<float>(dY, rows, cols, part, dbias, st);
+  const int64_t cols = dbias != nullptr && bj.nparts > 1 ? n_out : 0;
+  if (n + cols == 0) return cudaSuccess;
+  return bf ? launch_kernel(mx4_sum_kernel<__nv_bfloat16>, dim3(blocks_for(n + cols)), dim3(256), 0, st, true, (const float*)part, n, nsplit,
+                            (__nv_bfloat16*)dW, (const float*)bj.part, cols, bj.nparts, (__nv_bfloat16*)dbias)
+            : launch_kernel(mx4_sum_kernel<float>, dim3(blocks_for(n + cols)), dim3(256), 0, st, true, (const float*)part, n, nsplit,
+                            (float*)dW, (const float*)bj.part, cols, bj.nparts, (float*)dbias);
 }
 
 }  // namespace monarch

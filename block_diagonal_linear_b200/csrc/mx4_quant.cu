@@ -234,11 +234,10 @@ __device__ __forceinline__ void store_block(float* p, int n, const uint32_t (&v)
   }
 }
 
-// PIECE: bytes that rows of X are whole numbers of: 32, 16, or sizeof(T).  PAD: X is (nblocks, rows, pitch)
-// with zeros behind the end of a row; otherwise it has s's plain layout.
-template <typename T, int PIECE, bool PAD>
+// PIECE: bytes that rows of X are whole numbers of: 32, 16, or sizeof(T).
+template <typename T, int PIECE>
 __global__ void __launch_bounds__(kQThreads)
-    mx4_dequantise_kernel(Mx4View q, bool by_block, T* __restrict__ X, int64_t rtiles, int pitch) {
+    mx4_dequantise_kernel(Mx4View q, bool by_block, T* __restrict__ X, int64_t rtiles) {
   __shared__ __align__(16) uint8_t mem[PIECE == 32 ? 16 : sizeof(Tile<T>)];
   Tile<T>& tile = *(Tile<T>*)mem;
   ptx::griddep_wait();
@@ -260,9 +259,7 @@ __global__ void __launch_bounds__(kQThreads)
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[4 * i + e] = t[e];
     }
-    if (PAD) {
-      if (mine) store_block<32>(X + ((int64_t)b * s.rows + r) * pitch + kb * 32, pitch - kb * 32, v);
-    } else if (PIECE == 32) {
+    if (PIECE == 32) {
       if (mine) store_block<32>(X + plain_at(s, by_block, b, r, kb * 32), s.cols - kb * 32, v);
     } else {
       const int64_t r0 = rt * kQRows;
@@ -277,21 +274,20 @@ __global__ void __launch_bounds__(kQThreads)
 }
 
 bool rows_of_16_bytes(const Mx4Shape& s, int dtype) { return (int64_t)s.cols * (dtype == MONARCH_BF16 ? 2 : 4) % 16 == 0; }
-dim3 grid_for(const Mx4Shape& s, int64_t rtiles, int cols) {
-  return dim3((unsigned)(rtiles < (1 << 20) ? rtiles : (1 << 20)), (unsigned)((cols + 127) / 128), (unsigned)s.nblocks);
+dim3 grid_for(const Mx4Shape& s, int64_t rtiles) {
+  return dim3((unsigned)(rtiles < (1 << 20) ? rtiles : (1 << 20)), (unsigned)s.katoms(), (unsigned)s.nblocks);
 }
 
 template <typename T, bool VEC>
 cudaError_t quantise_t(const void* X, const Mx4Shape& s, bool by_block, uint8_t* codes, uint8_t* scales, cudaStream_t st) {
   const int64_t rt = s.ratoms() * (128 / kQRows);  // whole scale tiles
-  return launch_kernel(mx4_quantise_kernel<T, VEC>, grid_for(s, rt, s.cols), dim3(kQThreads), 0, st, true, (const T*)X, s, by_block,
+  return launch_kernel(mx4_quantise_kernel<T, VEC>, grid_for(s, rt), dim3(kQThreads), 0, st, true, (const T*)X, s, by_block,
                        codes, scales, rt);
 }
-template <typename T, int PIECE, bool PAD>
-cudaError_t dequantise_t(const Mx4View& q, bool by_block, void* X, int pitch, cudaStream_t st) {
+template <typename T, int PIECE>
+cudaError_t dequantise_t(const Mx4View& q, bool by_block, void* X, cudaStream_t st) {
   const int64_t rt = (q.s.rows + kQRows - 1) / kQRows;
-  return launch_kernel(mx4_dequantise_kernel<T, PIECE, PAD>, grid_for(q.s, rt, PAD ? pitch : q.s.cols), dim3(kQThreads), 0, st, true, q,
-                       by_block, (T*)X, rt, pitch);
+  return launch_kernel(mx4_dequantise_kernel<T, PIECE>, grid_for(q.s, rt), dim3(kQThreads), 0, st, true, q, by_block, (T*)X, rt);
 }
 
 }  // namespace
@@ -309,15 +305,11 @@ cudaError_t mx4_quantise(const void* X, const Mx4Shape& s, bool by_block, int dt
 template <typename T>
 static cudaError_t dequantise_any(const Mx4View& q, bool by_block, void* X, cudaStream_t st) {
   const int64_t row = (int64_t)q.s.cols * sizeof(T);
-  if (row % 32 == 0 && ((uintptr_t)X & 31u) == 0) return dequantise_t<T, 32, false>(q, by_block, X, 0, st);
-  return row % 16 == 0 ? dequantise_t<T, 16, false>(q, by_block, X, 0, st) : dequantise_t<T, (int)sizeof(T), false>(q, by_block, X, 0, st);
+  if (row % 32 == 0 && ((uintptr_t)X & 31u) == 0) return dequantise_t<T, 32>(q, by_block, X, st);
+  return row % 16 == 0 ? dequantise_t<T, 16>(q, by_block, X, st) : dequantise_t<T, (int)sizeof(T)>(q, by_block, X, st);
 }
 cudaError_t mx4_dequantise(const Mx4View& q, bool by_block, int dtype, void* X, cudaStream_t st) {
   return dtype == MONARCH_BF16 ? dequantise_any<__nv_bfloat16>(q, by_block, X, st) : dequantise_any<float>(q, by_block, X, st);
-}
-
-cudaError_t mx4_expand(const Mx4View& q, void* out, int pitch, cudaStream_t st) {
-  return dequantise_t<__nv_bfloat16, 32, true>(q, true, out, pitch, st);
 }
 
 }  // namespace monarch
