@@ -23,6 +23,7 @@ _DTYPES = {MONARCH_BF16: torch.bfloat16, MONARCH_F32: torch.float32}
 _CODES = {torch.bfloat16: MONARCH_BF16, torch.float32: MONARCH_F32}
 _byref = ctypes.byref
 _raw_stream = torch._C._cuda_getCurrentRawStream  # address of a device's current stream
+_current_device = torch._C._cuda_getDevice
 
 
 class Mx4:
@@ -32,16 +33,42 @@ class Mx4:
     ``by_block`` says which plain layout it came from: (nblocks, rows, cols), or (rows, nblocks * cols);
     ``dtype`` is that tensor's type ("bf16" / "f32")."""
 
-    __slots__ = ("codes", "scales", "rows", "nblocks", "cols", "by_block", "code")
+    # _hold: what keeps the memory alive; _pc, _ps: addresses of codes and scales; _index: their device;
+    # _layers: (rows, has_bias, code) -> dims of a layer with this weight and its workspace bytes
+    __slots__ = ("rows", "nblocks", "cols", "by_block", "code", "_hold", "_sizes", "_pc", "_ps", "_index", "_layers")
 
     def __init__(self, codes, scales, rows: int, nblocks: int, cols: int, by_block: bool, dtype):
-        self.rows, self.nblocks, self.cols, self.by_block = int(rows), int(nblocks), int(cols), bool(by_block)
-        self.code = dtype_code(dtype)
-        self.codes, self.scales = codes, scales
-        need = _buffer_bytes(_dims(self, self.code))
-        for name, t, n in (("codes", codes, need[0]), ("scales", scales, need[1])):
+        self._shape(int(rows), int(nblocks), int(cols), bool(by_block), dtype_code(dtype))
+        for name, t, n in (("codes", codes, self._sizes[0]), ("scales", scales, self._sizes[1])):
             if t.dtype != torch.uint8 or t.numel() != n:
                 raise ValueError("%s must be uint8 with %d elements" % (name, n))
+        self._index = -1 if not (codes.is_cuda and scales.is_cuda) else _device(codes, scales)
+        self._hold, self._pc, self._ps = (codes, scales), codes.data_ptr(), scales.data_ptr()
+
+    def _shape(self, rows, nblocks, cols, by_block, code):
+        self.rows, self.nblocks, self.cols, self.by_block, self.code = rows, nblocks, cols, by_block, code
+        self._layers = {}
+        self._sizes = _buffer_bytes(MonarchMx4Dims(rows, nblocks, cols, by_block, code))
+
+    @classmethod
+    def _new(cls, like, rows, nblocks, cols, by_block, code, stream):
+        """Uninitialised, on like's device: both buffers in one piece of memory."""
+        q = cls.__new__(cls)
+        q._shape(rows, nblocks, cols, by_block, code)
+        at = (q._sizes[0] + 511) & ~511
+        q._hold = _empty(like, (at + q._sizes[1],), torch.uint8, stream)
+        q._pc = q._hold.data_ptr()
+        q._ps = q._pc + at
+        q._index = like.get_device()
+        return q
+
+    @property
+    def codes(self):
+        return self._hold[0] if isinstance(self._hold, tuple) else self._hold[:self._sizes[0]]
+
+    @property
+    def scales(self):
+        return self._hold[1] if isinstance(self._hold, tuple) else self._hold[self._hold.numel() - self._sizes[1]:]
 
     @property
     def dtype(self) -> str:
@@ -58,14 +85,10 @@ class Mx4:
 
     @property
     def nbytes(self) -> int:
-        return self.codes.numel() + self.scales.numel()
+        return sum(self._sizes)
 
     def __repr__(self):
         return "Mx4(shape=%s, nblocks=%d, dtype=%s)" % (tuple(self.shape), self.nblocks, self.dtype)
-
-
-def _dims(q, code: int) -> MonarchMx4Dims:
-    return MonarchMx4Dims(q.rows, q.nblocks, q.cols, q.by_block, code)
 
 
 def _buffer_bytes(d) -> tuple:
@@ -94,6 +117,13 @@ def _device(*ts) -> int:
     return device
 
 
+def _together(device, *qs):
+    """Raises unless every Mx4 lies on `device`."""
+    for q in qs:
+        if q is not None and q._index != device:
+            raise ValueError("an Mx4 on %s and tensors on cuda:%d: one call takes one device's" % (q.device, device))
+
+
 def _empty(like, shape, dtype, stream):
     """Memory on like's device for work on `stream` (None: that device's current one)."""
     if stream is None:
@@ -105,7 +135,7 @@ def _empty(like, shape, dtype, stream):
 def _call(name, fn, device, stream, *args):
     """fn, the C entry point `name`, on args and the stream handle, with `device` the current one."""
     s = _raw_stream(device) if stream is None else stream.cuda_stream
-    if device == torch.cuda.current_device():
+    if device == _current_device():
         rc = fn(*args, s)
     else:
         with torch.cuda.device(device):
@@ -138,27 +168,24 @@ def mx4_quantise(X, nblocks: int | None = None, stream=None) -> Mx4:
     """X in MX4.  A 3-D X is a weight (nblocks, out_blk, in_blk); a 2-D X (rows, nblocks * cols) holds
     activations of `nblocks` blocks (default 1).  Scales never span two rows or two blocks."""
     code = _code(X, "X")
-    by_block = X.dim() == 3
+    shape = X.shape
+    by_block = len(shape) == 3
     if by_block:
-        nb, rows, cols = X.shape
+        nb, rows, cols = shape
         if nblocks is not None and nblocks != nb:
             raise ValueError("X has %d blocks, nblocks is %d" % (nb, nblocks))
-    elif X.dim() == 2:
+    elif len(shape) == 2:
         nb = 1 if nblocks is None else int(nblocks)
-        rows, width = X.shape
+        rows, width = shape
         if nb <= 0 or width % nb:
             raise ValueError("%d columns do not divide into %d blocks" % (width, nb))
         cols = width // nb
     else:
-        raise ValueError("X must have 2 or 3 dimensions, got %d" % X.dim())
+        raise ValueError("X must have 2 or 3 dimensions, got %d" % len(shape))
     device = _device(X)
-    d = MonarchMx4Dims(rows, nb, cols, by_block, code)
-    nc, ns = _buffer_bytes(d)
-    q = Mx4.__new__(Mx4)
-    q.codes, q.scales = _empty(X, (nc,), torch.uint8, stream), _empty(X, (ns,), torch.uint8, stream)
-    q.rows, q.nblocks, q.cols, q.by_block, q.code = rows, nb, cols, by_block, code
-    _call("monarch_mx4_quantise", lib().monarch_mx4_quantise, device, stream, X.data_ptr(), _byref(d), q.codes.data_ptr(),
-          q.scales.data_ptr())
+    q = Mx4._new(X, rows, nb, cols, by_block, code, stream)
+    _call("monarch_mx4_quantise", lib().monarch_mx4_quantise, device, stream, X.data_ptr(),
+          _byref(MonarchMx4Dims(rows, nb, cols, by_block, code)), q._pc, q._ps)
     return q
 
 
@@ -167,12 +194,14 @@ def mx4_dequantise(q: Mx4, dtype=None, out=None, stream=None):
     code = q.code if dtype is None else dtype_code(dtype)
     dt = _DTYPES[code]
     if out is None:
-        out = _empty(q.codes, q.shape, dt, stream)
+        like = q._hold[0] if isinstance(q._hold, tuple) else q._hold
+        out = _empty(like, q.shape, dt, stream)
     elif tuple(out.shape) != tuple(q.shape) or out.dtype != dt:
         raise ValueError("out must be %s of shape %s" % (dt, tuple(q.shape)))
-    device = _device(q.codes, q.scales, out)
-    _call("monarch_mx4_dequantise", lib().monarch_mx4_dequantise, device, stream, q.codes.data_ptr(), q.scales.data_ptr(),
-          _byref(_dims(q, code)), out.data_ptr())
+    device = _device(out)
+    _together(device, q)
+    _call("monarch_mx4_dequantise", lib().monarch_mx4_dequantise, device, stream, q._pc, q._ps,
+          _byref(MonarchMx4Dims(q.rows, q.nblocks, q.cols, q.by_block, code)), out.data_ptr())
     return out
 
 
@@ -189,6 +218,18 @@ def _activations(X, W):
 def _expect(t, name, shape, dtype):
     if t is not None and (t.shape != shape or t.dtype != dtype):
         raise ValueError("%s must be %s of shape %s, is %s of shape %s" % (name, dtype, shape, t.dtype, tuple(t.shape)))
+
+
+def _layer(W, rows, has_bias, code):
+    """(dims by reference, forward workspace bytes, backward workspace bytes) of a layer with weight W."""
+    plan = W._layers.get((rows, has_bias, code))
+    if plan is None:
+        if len(W._layers) >= 64:  # a serving loop sees few batch sizes; any number must not pile up
+            W._layers.clear()
+        d, L = _byref(MonarchMx4LinearDims(rows, W.nblocks, W.cols, W.rows, has_bias, code)), lib()
+        plan = W._layers[(rows, has_bias, code)] = (d, L.monarch_mx4_linear_wfwd_workspace_bytes(d),
+                                                    L.monarch_mx4_linear_bwd_workspace_bytes(d))
+    return plan
 
 
 def mx4_linear_workspace_bytes(rows: int, nblocks: int, in_blk: int, out_blk: int, dtype="bf16", bias: bool = False,
@@ -218,22 +259,25 @@ def mx4_linear_fwd(X, W: Mx4, bias=None, Y=None, dtype=None, workspace=None, str
         _expect(X, "X", (rows, W.nblocks * W.cols), X.dtype)
     dt = _DTYPES[code]
     n_out = W.nblocks * W.rows
-    _expect(bias, "bias", (n_out,), dt)
+    if bias is not None:
+        _expect(bias, "bias", (n_out,), dt)
     if Y is None:
-        Y = _empty(W.codes, (rows, n_out), dt, stream)
+        like = X if not both else X._hold[0] if isinstance(X._hold, tuple) else X._hold
+        Y = _empty(like, (rows, n_out), dt, stream)
     else:
         _expect(Y, "Y", (rows, n_out), dt)
-    d = _byref(MonarchMx4LinearDims(rows, W.nblocks, W.cols, W.rows, bias is not None, code))
-    L = lib()
+    d, need, _ = _layer(W, rows, bias is not None, code)
     if both:
-        device = _device(X.codes, X.scales, W.codes, W.scales, bias, Y)
-        _call("monarch_mx4_linear_fwd", L.monarch_mx4_linear_fwd, device, stream, X.codes.data_ptr(), X.scales.data_ptr(),
-              W.codes.data_ptr(), W.scales.data_ptr(), _p(bias), d, Y.data_ptr())
+        device = _device(Y, bias)
+        _together(device, W, X)
+        _call("monarch_mx4_linear_fwd", lib().monarch_mx4_linear_fwd, device, stream, X._pc, X._ps, W._pc, W._ps, _p(bias), d,
+              Y.data_ptr())
     else:
-        device = _device(X, W.codes, W.scales, bias, Y, workspace)
-        workspace, wp, wn = _workspace(workspace, L.monarch_mx4_linear_wfwd_workspace_bytes(d), X, stream)
-        _call("monarch_mx4_linear_wfwd", L.monarch_mx4_linear_wfwd, device, stream, X.data_ptr(), W.codes.data_ptr(),
-              W.scales.data_ptr(), _p(bias), d, Y.data_ptr(), wp, wn)
+        device = _device(X, Y, bias, workspace)
+        _together(device, W)
+        workspace, wp, wn = _workspace(workspace, need, X, stream)
+        _call("monarch_mx4_linear_wfwd", lib().monarch_mx4_linear_wfwd, device, stream, X.data_ptr(), W._pc, W._ps, _p(bias), d,
+              Y.data_ptr(), wp, wn)
     return Y
 
 
@@ -269,13 +313,13 @@ def mx4_linear_bwd(dY, X, W, bias: bool = False, need_dX: bool = True, dX=None, 
         dbias = None
     elif dbias is None:
         dbias = _empty(dY, (n_out,), dt, stream)
-    xc, xs = (X.codes, X.scales) if X is not None else (None, None)
-    device = _device(dY, W.codes, W.scales, xc, xs, dX, dW, dbias, workspace)
-    d = _byref(MonarchMx4LinearDims(rows, W.nblocks, W.cols, W.rows, bool(bias), code))
-    L = lib()
-    workspace, wp, wn = _workspace(workspace, L.monarch_mx4_linear_bwd_workspace_bytes(d), dY, stream)
-    _call("monarch_mx4_linear_bwd", L.monarch_mx4_linear_bwd, device, stream, dY.data_ptr(), _p(xc), _p(xs), W.codes.data_ptr(),
-          W.scales.data_ptr(), d, _p(dX), _p(dW), _p(dbias), wp, wn)
+    device = _device(dY, dX, dW, dbias, workspace)
+    _together(device, W, X)
+    d, _, need = _layer(W, rows, bool(bias), code)
+    workspace, wp, wn = _workspace(workspace, need, dY, stream)
+    xc, xs = (None, None) if X is None else (X._pc, X._ps)
+    _call("monarch_mx4_linear_bwd", lib().monarch_mx4_linear_bwd, device, stream, dY.data_ptr(), xc, xs, W._pc, W._ps, d, _p(dX),
+          _p(dW), _p(dbias), wp, wn)
     return dX, dW, dbias
 
 
@@ -297,8 +341,8 @@ def mx4_fwd(X, R: Mx4, L: Mx4, shape: dict, Y=None, workspace=None, stream=None)
         _expect(Y, "Y", (rows, nb2 * out2), dt)
     d = _byref(MonarchDims(rows, nb1, in1, out1, nb2, in2, out2, int(shape.get("out_transpose", 1)), code))
     lb = lib()
-    device = _device(X, R.codes, R.scales, L.codes, L.scales, Y, workspace)
+    device = _device(X, Y, workspace)
+    _together(device, R, L)
     workspace, wp, wn = _workspace(workspace, lb.monarch_mx4_fwd_workspace_bytes(d), X, stream)
-    _call("monarch_mx4_fwd", lb.monarch_mx4_fwd, device, stream, X.data_ptr(), R.codes.data_ptr(), R.scales.data_ptr(),
-          L.codes.data_ptr(), L.scales.data_ptr(), d, Y.data_ptr(), wp, wn)
+    _call("monarch_mx4_fwd", lb.monarch_mx4_fwd, device, stream, X.data_ptr(), R._pc, R._ps, L._pc, L._ps, d, Y.data_ptr(), wp, wn)
     return Y
