@@ -102,6 +102,45 @@ __device__ __forceinline__ void values8(uint32_t w, uint32_t byte, uint32_t (&v)
   v[3] = __byte_perm(p[2], p[3], 0x7632);
 }
 
+// A warp's 32 rows x 128 bytes of results: written to shared memory as 128-byte swizzled lines (one row a
+// lane; the layout that a TMA store of 32 rows takes), and from there to rows of any alignment.
+template <typename T, int CC>
+__device__ __forceinline__ void slab_write(uint32_t slab, int lane, const uint32_t (&v)[CC]) {
+  static_assert(CC * sizeof(T) == 128, "a row is 128 bytes");
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const uint32_t at = slab + lane * 128 + (((uint32_t)q ^ (uint32_t)(lane & 7)) << 4);
+    if (sizeof(T) == 2)
+      ptx::st_shared_v4(at, ptx::pack_bf16x2(__uint_as_float(v[(8 * q + 0) % CC]), __uint_as_float(v[(8 * q + 1) % CC])),
+                        ptx::pack_bf16x2(__uint_as_float(v[(8 * q + 2) % CC]), __uint_as_float(v[(8 * q + 3) % CC])),
+                        ptx::pack_bf16x2(__uint_as_float(v[(8 * q + 4) % CC]), __uint_as_float(v[(8 * q + 5) % CC])),
+                        ptx::pack_bf16x2(__uint_as_float(v[(8 * q + 6) % CC]), __uint_as_float(v[(8 * q + 7) % CC])));
+    else
+      ptx::st_shared_v4(at, v[(4 * q) % CC], v[(4 * q + 1) % CC], v[(4 * q + 2) % CC], v[(4 * q + 3) % CC]);
+  }
+}
+// rows, cols: how many of the 32 and CC are stored; lanes along the columns, eight rows in flight (row by
+// row the loads' latency bounded products of odd widths).
+template <typename T, int CC>
+__device__ __forceinline__ void slab_store(const uint8_t* slab, int lane, T* dst, int64_t pitch, int rows, int cols) {
+#pragma unroll
+  for (int r0 = 0; r0 < 32; r0 += 8) {
+    T v[8][CC / 32];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int e = 0; e < CC / 32; ++e) {
+        const int byte = (e * 32 + lane) * (int)sizeof(T);
+        v[i][e] = *(const T*)(slab + (r0 + i) * 128 + (((byte >> 4) ^ i) << 4) + (byte & 15));
+      }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int e = 0; e < CC / 32; ++e)
+        if (r0 + i < rows && e * 32 + lane < cols) dst[(r0 + i) * pitch + e * 32 + lane] = v[i][e];
+  }
+}
+
 }  // namespace mx4
 
 // ---- launchers (cudaError_t; arguments already checked) ----

@@ -17,7 +17,8 @@
 // index (rows of 128 swizzled bytes) or its M / N index (chunks of 64 x 64); all tensor maps are per
 // block, so tiles that hang over a block's edge read zeros and write nothing there.  A long K with few
 // tiles is split; the parts are written in fp32 and summed in order.
-// Roles: warp 0 TMA producer, warp 1 MMA issuer (of the pair's first CTA), warps 2..5 epilogue.
+// Roles: warp 0 TMA producer, warp 1 MMA issuer (of the pair's first CTA), warps 2..9 epilogue (two warps a
+// TMEM lane quadrant, alternate 128-byte chunks of columns, each staging and storing its own 32 rows).
 #include <algorithm>
 
 #include "mx4.cuh"
@@ -27,16 +28,16 @@ namespace monarch {
 
 namespace {
 
-constexpr int kThreads = 192;
-constexpr int kEpiWarps = 4;
-constexpr int kStagingChunk = 128 * 128;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kSlab = 32 * 128;  // a warp's 32 rows x 128 bytes of results
 
 struct GJob {
   int nb, mtiles, ntiles, nsplit;
   int64_t units;
   int64_t m;           // rows of D, for the epilogue without TMA
   int n;               // columns of D per block
-  int64_t d_b, d_m;    // D strides (elements) of a block and a row, for the epilogue without TMA
+  int64_t d_b, d_m, d_s;  // D strides (elements) of a block, a row and a split, for the epilogue without TMA
   int nk, parts;       // K stages of one part; parts of A
   int stages_per_split;
   int a_chunked, b_chunked;  // inner index M / N: the map is 4-D and both 64-wide chunks are one box
@@ -51,7 +52,8 @@ struct GCfg {
   static constexpr int A_BYTES = 128 * 128, B_BYTES = 128 * 128;  // this CTA's 128 rows of each, K = 64
   static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int NSTAGE = 5;
-  static constexpr int SMEM_BYTES = 2 * kStagingChunk + NSTAGE * STAGE + 2048 + 1024;
+  static constexpr int TAIL = 5120;
+  static constexpr int SMEM_BYTES = kEpiWarps * kSlab + NSTAGE * STAGE + TAIL + 1024;
   static constexpr int TMEM_COLS = 2 * BN;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
 };
@@ -62,9 +64,9 @@ struct GBars {
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort_flag;
-  float bias[256];
+  alignas(16) float bias[kEpiWarps][128];  // of a warp's chunks of the current tile
 };
-static_assert(sizeof(GBars) <= 2048, "bars");
+static_assert(sizeof(GBars) <= 5120, "bars");
 
 struct GUnit {
   int b, mt, nt, split;
@@ -122,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* stg = smem;
-  uint8_t* ring = smem + 2 * kStagingChunk;
+  uint8_t* ring = smem + kEpiWarps * kSlab;
   GBars* bars = (GBars*)(ring + C::NSTAGE * C::STAGE);
   int* abort_flag = &bars->abort_flag;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -245,35 +247,44 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) wait_mma_done(&bars->mma_done, abort_flag, status);
     __syncwarp();
   } else {
-    // ================================================================ epilogue (4 warps a CTA)
+    // ================================================================ epilogue (8 warps a CTA)
     constexpr int CC = 128 / (int)sizeof(T);  // columns of a 128-byte chunk
-    constexpr int NCH = C::BN / CC;
-    const int quad = warp & 3;
-    const int r = quad * 32 + lane;
+    constexpr int NCH = C::BN / CC, MINE = NCH / 2, NB = MINE * CC / 32;
+    const int ew = warp - 2, quad = warp & 3, half = ew >> 2;  // warps 2..5: even chunks, 6..9: odd ones
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-    const int et = threadIdx.x - 64;
-    const bool leader = et == 0;
-    const uint32_t stg_s = ptx::smem_u32(stg);
+    uint8_t* slab = stg + ew * kSlab;
+    const uint32_t slab_s = ptx::smem_u32(slab);
+    float* bias_s = bars->bias[ew];
     const uint32_t acc_empty0 = PAIR ? ptx::mapa_shared(ptx::smem_u32(&bars->acc_empty[0]), 0) : 0u;
-    uint32_t n = 0, chunk_n = 0;
-    bool ok = true;
-    for (int64_t u = cl; u < job.units && ok; u += ncl, ++n) {
+    float next_bias[NB];
+    auto fetch_bias = [&](int64_t u) {
+      const GUnit c = unit_at(job, u);
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        const int col = c.nt * C::BN + ((32 * i / CC) * 2 + half) * CC + (32 * i) % CC + lane;
+        next_bias[i] = u < job.units && col < job.n ? mx4::load(bias + (int64_t)c.b * job.n + col) : 0.f;
+      }
+    };
+    if (bias != nullptr) fetch_bias(cl);
+    uint32_t n = 0;
+    for (int64_t u = cl; u < job.units; u += ncl, ++n) {
       const GUnit c = unit_at(job, u);
       const int slot = n & 1;
       const int n0 = c.nt * C::BN;
-      const int64_t m0 = (int64_t)c.mt * C::BM + (int64_t)rank * 128;
-      const int blk = c.split * job.nb + c.b;
+      const int64_t m0 = (int64_t)c.mt * C::BM + (int64_t)rank * 128 + quad * 32;  // this warp's rows
       if (bias != nullptr) {
-        ptx::named_bar_sync(1, kEpiWarps * 32);  // the previous tile's bias has been read
-        for (int i = et; i < C::BN; i += kEpiWarps * 32)
-          bars->bias[i] = n0 + i < job.n ? mx4::load(bias + (int64_t)c.b * job.n + n0 + i) : 0.f;
+        __syncwarp();  // the previous tile's has been read
+#pragma unroll
+        for (int i = 0; i < NB; ++i) bias_s[32 * i + lane] = next_bias[i];
+        __syncwarp();
+        fetch_bias(u + ncl);  // asked for a tile ahead
       }
-      // one verdict for the four warps: none may leave while another waits for it at a barrier
-      ok = ptx::named_bar_all(1, kEpiWarps * 32, wait_or_abort(&bars->acc_full[slot], (n >> 1) & 1, abort_flag, status));
-      if (!ok) break;
+      if (!all_wait_or_abort(&bars->acc_full[slot], (n >> 1) & 1, abort_flag, status)) break;
       ptx::tc_fence_after();
       const uint32_t tb = tmem + lane_off + slot * C::BN;
-      for (int ch = 0; ch < NCH; ++ch) {
+#pragma unroll 1
+      for (int i = 0; i < MINE; ++i) {
+        const int ch = 2 * i + half;
         if (n0 + ch * CC >= job.n || m0 >= job.m) break;  // behind the block's last column or row
         uint32_t v[CC];
 #pragma unroll
@@ -286,45 +297,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tmem_wait_ld();
         if (bias != nullptr) {
 #pragma unroll
-          for (int e = 0; e < CC; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) + bars->bias[ch * CC + e]);
+          for (int e = 0; e < CC; e += 4) {
+            const float4 f = *(const float4*)(bias_s + i * CC + e);
+            v[e] = __float_as_uint(__uint_as_float(v[e]) + f.x);
+            v[e + 1] = __float_as_uint(__uint_as_float(v[e + 1]) + f.y);
+            v[e + 2] = __float_as_uint(__uint_as_float(v[e + 2]) + f.z);
+            v[e + 3] = __float_as_uint(__uint_as_float(v[e + 3]) + f.w);
+          }
         }
-        const int sbuf = chunk_n++ & 1;
-        if (C::TMA_OUT && leader) ptx::bulk_wait_read_allbut1();  // what last left this buffer has been read
-        ptx::named_bar_sync(2, kEpiWarps * 32);
-        const uint32_t base = stg_s + sbuf * kStagingChunk + r * 128;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const uint32_t at = base + (((uint32_t)q ^ (uint32_t)(r & 7)) << 4);
-          if (sizeof(T) == 2)
-            ptx::st_shared_v4(at, ptx::pack_bf16x2(__uint_as_float(v[(8 * q + 0) % CC]), __uint_as_float(v[(8 * q + 1) % CC])),
-                              ptx::pack_bf16x2(__uint_as_float(v[(8 * q + 2) % CC]), __uint_as_float(v[(8 * q + 3) % CC])),
-                              ptx::pack_bf16x2(__uint_as_float(v[(8 * q + 4) % CC]), __uint_as_float(v[(8 * q + 5) % CC])),
-                              ptx::pack_bf16x2(__uint_as_float(v[(8 * q + 6) % CC]), __uint_as_float(v[(8 * q + 7) % CC])));
-          else
-            ptx::st_shared_v4(at, v[(4 * q) % CC], v[(4 * q + 1) % CC], v[(4 * q + 2) % CC], v[(4 * q + 3) % CC]);
-        }
+        if (C::TMA_OUT && lane == 0) ptx::bulk_wait_read_all();  // what last left the slab has been read
+        __syncwarp();
+        mx4::slab_write<T, CC>(slab_s, lane, v);
         if (C::TMA_OUT) {
           ptx::fence_proxy_async_smem();
-          ptx::named_bar_sync(2, kEpiWarps * 32);
-          if (leader) {
-            ptx::tma_store_3d(&tmD, stg + sbuf * kStagingChunk, n0 + ch * CC, blk, (int)m0);
+          __syncwarp();
+          if (lane == 0) {
+            ptx::tma_store_4d(&tmD, slab, n0 + ch * CC, c.b, (int)m0, c.split);
             ptx::bulk_commit_group();
           }
-        } else {
-          // a row pitch that is no multiple of 16 bytes: each warp writes its own 32 rows
+        } else {  // a row pitch that is no multiple of 16 bytes
           __syncwarp();
-          const int cols = job.n - n0 - ch * CC;
-          for (int rr = 0; rr < 32; ++rr) {
-            const int64_t row = m0 + quad * 32 + rr;
-            if (row >= job.m) break;
-            const uint8_t* src = stg + sbuf * kStagingChunk + (quad * 32 + rr) * 128;
-            T* dst = D + row * job.d_m + blk * job.d_b + n0 + ch * CC;
-#pragma unroll
-            for (int e = 0; e < CC / 32; ++e) {
-              const int col = e * 32 + lane, byte = col * (int)sizeof(T);
-              if (col < cols) dst[col] = *(const T*)(src + (((byte >> 4) ^ (rr & 7)) << 4) + (byte & 15));
-            }
-          }
+          mx4::slab_store<T, CC>(slab, lane, D + c.split * job.d_s + m0 * job.d_m + c.b * job.d_b + n0 + ch * CC, job.d_m,
+                                 (int)min((int64_t)32, job.m - m0), job.n - n0 - ch * CC);
         }
       }
       ptx::tc_fence_before();
@@ -336,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::mbar_arrive_cluster(acc_empty0 + (uint32_t)(slot * sizeof(uint64_t)));
       }
     }
-    if (C::TMA_OUT && leader) ptx::bulk_wait_all();
+    if (C::TMA_OUT && lane == 0) ptx::bulk_wait_all();
   }
 
   ptx::tc_fence_before();
@@ -527,24 +521,34 @@ __global__ void __launch_bounds__(256)
     expand_tile(e1, blk - e0.blocks);
 }
 
-// What is left to add at the end, parts in order: out[e] over nsplit parts of n, dbias[c] over nparts of cols.
+// What is left to add at the end, parts in order: out[e] over nsplit parts of n values (+ bias[e % width]),
+// dbias[c] over nparts parts of cols.
+struct SumJob {
+  const float* part;
+  int64_t n;
+  int nsplit;
+  const void* bias;
+  int64_t width;
+  const float* bpart;
+  int64_t cols, nparts;
+};
 template <typename T>
-__global__ void __launch_bounds__(256)
-    mx4_sum_kernel(const float* __restrict__ part, int64_t n, int nsplit, T* __restrict__ out, const float* __restrict__ bpart,
-                   int64_t cols, int64_t nparts, T* __restrict__ dbias) {
+__global__ void __launch_bounds__(256) mx4_sum_kernel(const __grid_constant__ SumJob j, T* __restrict__ out, T* __restrict__ dbias) {
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
-  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < n + cols; e += (int64_t)gridDim.x * 256) {
-    const bool b = e >= n;
-    const float* p = b ? bpart + (e - n) : part + e;
-    const int64_t step = b ? cols : n, m = b ? nparts : nsplit;
+  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < j.n + j.cols; e += (int64_t)gridDim.x * 256) {
+    const bool b = e >= j.n;
+    const float* p = b ? j.bpart + (e - j.n) : j.part + e;
+    const int64_t step = b ? j.cols : j.n, m = b ? j.nparts : j.nsplit;
     float acc = 0.f;
 #pragma unroll 8
     for (int64_t s = 0; s < m; ++s) acc += p[s * step];
-    if (b)
-      st_from_f32(dbias + (e - n), acc);
-    else
+    if (b) {
+      st_from_f32(dbias + (e - j.n), acc);
+    } else {
+      if (j.bias != nullptr) acc += mx4::load((const T*)j.bias + e % j.width);
       st_from_f32(out + e, acc);
+    }
   }
 }
 
@@ -554,6 +558,7 @@ unsigned blocks_for(int64_t threads) {
 }
 
 int up(int v, int to) { return (v + to - 1) / to * to; }
+int64_t up64(int64_t v) { return (v + 63) / 64 * 64; }
 size_t al256(size_t b) { return (b + 255) & ~size_t(255); }
 
 // ---------------------------------------------------------------- tensor maps
@@ -591,34 +596,42 @@ bool mnmajor_map(CUtensorMap* m, const Operand& o, int* chunked) {
   return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, o.p, dims, st, box);
 }
 
-// D: columns n, rows m, `batch` blocks; strides in elements.
+// D: columns n, rows m of nb blocks; strides in elements of a row, a block and a split.
 struct Result {
   void* p;
   int64_t m;
-  int n;
-  int64_t batch, d_m, d_b;
+  int n, nb;
+  int64_t d_m, d_b, d_s;
 };
 
 struct Plan {
   bool pair;
-  int nsplit, per_split, stages;
+  int nsplit, per_split;
 };
-// 256 x 256 tiles where they fill at least three quarters of the SM pairs (measured: see the table of
-// tiles in the design notes), else 128 x 128; K is split while the tiles leave SMs idle, down to 8
-// stages of 64 a part.
-Plan plan_for(int64_t m, int n, int nb, int nk, bool may_split) {
-  Plan p;
-  const int64_t big = (m + 255) / 256 * ((n + 255) / 256) * nb, pairs = num_sms() / 2;
-  const int64_t want = may_split && nk >= 16 ? std::min<int64_t>(nk / 8, 1 << 10) : 1;
-  p.stages = nk;
-  p.pair = big * want >= pairs * 3 / 4;
-  const int64_t tiles = p.pair ? big : (m + 127) / 128 * ((n + 127) / 128) * nb, slots = p.pair ? pairs : num_sms();
-  int64_t s = may_split ? slots / tiles : 1;
-  s = std::max<int64_t>(1, std::min(s, want));
-  p.per_split = (int)((nk + s - 1) / s);
-  p.nsplit = (nk + p.per_split - 1) / p.per_split;
-  return p;
+// 256 x 256 tiles on pairs or 128 x 128 on single CTAs, and how many parts of K: whichever takes the least
+// time by this count of microseconds: rounds over the SMs, 0.40 (pair) or 0.33 a stage of 64 inputs (8192 x 1024 ->
+// 4096: 52.4 us on pairs, 81 on single CTAs), a tile's start and epilogue, and, when K is split, the partial
+// sums' way out and back.
+Plan plan_for(int64_t m, int n, int nb, int nk) {
+  Plan best{};
+  double least = 1e30;
+  for (int pair = 0; pair < 2; ++pair) {
+    const int bm = pair ? 256 : 128;
+    const int64_t tiles = (m + bm - 1) / bm * ((n + bm - 1) / bm) * nb, slots = pair ? num_sms() / 2 : num_sms();
+    for (int want = 1; want <= 64 && want * 4 <= std::max(nk, 4); want *= 2) {
+      const int per = (nk + want - 1) / want, ns = (nk + per - 1) / per;
+      const int64_t rounds = (tiles * ns + slots - 1) / slots;
+      double t = (double)rounds * (per * (pair ? 0.40 : 0.33) + (pair ? 2.0 : 1.2));
+      if (ns > 1) t += 2.5 + (double)m * n * nb * 4 * (ns + 1) / 5e6;
+      if (t < least) {
+        least = t;
+        best = Plan{pair != 0, ns, per};
+      }
+    }
+  }
+  return best;
 }
+size_t part_bytes(const Plan& p, int64_t results) { return p.nsplit > 1 ? (size_t)p.nsplit * (size_t)results * 4 : 0; }
 
 template <class C>
 cudaError_t launch(const Operand& a, const Operand& b, const Result& d, const void* bias, GJob j, int* status, cudaStream_t st) {
@@ -629,10 +642,10 @@ cudaError_t launch(const Operand& a, const Operand& b, const Result& d, const vo
       !(C::B_MN ? mnmajor_map(&mB, b, &j.b_chunked) : kmajor_map(&mB, b)))
     return cudaErrorInvalidValue;
   if (C::TMA_OUT) {
-    const cuuint64_t dims[3] = {(cuuint64_t)d.n, (cuuint64_t)d.batch, (cuuint64_t)d.m};
-    const cuuint64_t strides[2] = {(cuuint64_t)d.d_b * sizeof(T), (cuuint64_t)d.d_m * sizeof(T)};
-    const cuuint32_t box[3] = {(cuuint32_t)(128 / sizeof(T)), 1, 128};
-    if (!encode(&mD, sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, d.p, dims, strides, box))
+    const cuuint64_t dims[4] = {(cuuint64_t)d.n, (cuuint64_t)d.nb, (cuuint64_t)d.m, (cuuint64_t)j.nsplit};
+    const cuuint64_t strides[3] = {(cuuint64_t)d.d_b * sizeof(T), (cuuint64_t)d.d_m * sizeof(T), (cuuint64_t)d.d_s * sizeof(T)};
+    const cuuint32_t box[4] = {(cuuint32_t)(128 / sizeof(T)), 1, 32, 1};
+    if (!encode(&mD, sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, d.p, dims, strides, box))
       return cudaErrorInvalidValue;
   } else {
     mD = mA;  // unused
@@ -672,10 +685,11 @@ cudaError_t gemm(const Operand& a, const Operand& b, const Result& d, const void
   j.n = d.n;
   j.d_b = d.d_b;
   j.d_m = d.d_m;
+  j.d_s = d.d_s;
   j.nk = (int)((k + 63) / 64);
   j.parts = parts;
   j.stages_per_split = p.per_split;
-  const bool tma = d.d_m * sizeof(T) % 16 == 0 && d.d_b * sizeof(T) % 16 == 0;
+  const bool tma = d.d_m * sizeof(T) % 16 == 0 && d.d_b * sizeof(T) % 16 == 0 && d.d_s * sizeof(T) % 16 == 0;
   if (p.pair)
     return tma ? launch<GCfg<true, A_MN, B_MN, T, true>>(a, b, d, bias, j, status, st)
                : launch<GCfg<true, A_MN, B_MN, T, false>>(a, b, d, bias, j, status, st);
@@ -690,13 +704,13 @@ size_t staged_bytes(const Mx4Linear& d, int blk) {
   return direct(d.dtype, blk) ? 0 : al256((size_t)d.rows * d.nb * parts_of(d.dtype) * up(blk, 64) * 2);
 }
 size_t expanded_bytes(const Mx4Shape& s) { return al256((size_t)s.nblocks * s.rows * up(s.cols, 64) * 2); }
-Plan dw_plan(const Mx4Linear& d) {
-  return plan_for(d.out, d.in, d.nb, (int)((d.rows + 63) / 64) * parts_of(d.dtype), true);
-}
-size_t dw_part_bytes(const Mx4Linear& d) {
-  const Plan p = dw_plan(d);
-  return p.nsplit > 1 ? al256((size_t)p.nsplit * d.nb * d.out * d.in * 4) : 0;
-}
+int stages(int64_t k, int dtype) { return (int)((k + 63) / 64) * parts_of(dtype); }
+Plan fwd_plan(const Mx4Linear& d) { return plan_for(d.rows, d.out, d.nb, stages(d.in, d.dtype)); }
+Plan dx_plan(const Mx4Linear& d) { return plan_for(d.rows, d.in, d.nb, stages(d.out, d.dtype)); }
+Plan dw_plan(const Mx4Linear& d) { return plan_for(d.out, d.in, d.nb, stages(d.rows, d.dtype)); }
+size_t fwd_part_bytes(const Mx4Linear& d) { return al256(part_bytes(fwd_plan(d), d.rows * d.nb * d.out)); }
+size_t dx_part_bytes(const Mx4Linear& d) { return al256(part_bytes(dx_plan(d), d.rows * d.nb * d.in)); }
+size_t dw_part_bytes(const Mx4Linear& d) { return al256(part_bytes(dw_plan(d), (int64_t)d.nb * d.out * d.in)); }
 
 ExpandJob expand_job(const Mx4View& q, void* out) {
   ExpandJob j;
@@ -741,7 +755,29 @@ Operand expanded(const void* p, const Mx4Shape& s) {
   return Operand{p, pitch, s.rows, s.nblocks, pitch, (int64_t)pitch * s.rows};
 }
 
-// Backward scratch: the operands in bf16, split sums of dW, parts of dbias.
+// One product into `out` (results in the order of `r`), or into fp32 parts when K is split.
+template <bool A_MN, bool B_MN>
+cudaError_t product(const Operand& a, const Operand& b, Result r, const void* bias, const Mx4Linear& d, int64_t k, const Plan& p,
+                    float* part, int64_t results, int* status, cudaStream_t st) {
+  const int parts = parts_of(d.dtype);
+  r.d_s = results;
+  if (p.nsplit > 1) {
+    r.p = part;
+    return gemm<A_MN, B_MN, float>(a, b, r, nullptr, d.nb, k, parts, p, status, st);
+  }
+  r.d_s = up64(results);  // one part: any stride that a tensor map takes
+  return d.dtype == MONARCH_BF16 ? gemm<A_MN, B_MN, __nv_bfloat16>(a, b, r, bias, d.nb, k, parts, p, status, st)
+                                 : gemm<A_MN, B_MN, float>(a, b, r, bias, d.nb, k, parts, p, status, st);
+}
+cudaError_t sum(const Mx4Linear& d, const SumJob& j, void* out, void* dbias, cudaStream_t st) {
+  if (j.n + j.cols == 0) return cudaSuccess;
+  const dim3 grid(blocks_for(j.n + j.cols));
+  return d.dtype == MONARCH_BF16
+             ? launch_kernel(mx4_sum_kernel<__nv_bfloat16>, grid, dim3(256), 0, st, true, j, (__nv_bfloat16*)out, (__nv_bfloat16*)dbias)
+             : launch_kernel(mx4_sum_kernel<float>, grid, dim3(256), 0, st, true, j, (float*)out, (float*)dbias);
+}
+
+// Scratch: the operands in bf16, split sums, parts of dbias.  dX's split sums are joined before dW's are made.
 struct BwdWs {
   size_t w, x, dy, part, bias, total;
 };
@@ -751,26 +787,29 @@ BwdWs bwd_layout(const Mx4Linear& d) {
   l.x = l.w + expanded_bytes(d.w());
   l.dy = l.x + expanded_bytes(d.x());
   l.part = l.dy + staged_bytes(d, d.out);
-  l.bias = l.part + dw_part_bytes(d);
+  l.bias = l.part + std::max(dx_part_bytes(d), dw_part_bytes(d));
   l.total = l.bias + bias_part_bytes(d);
   return l;
 }
 
 }  // namespace
 
-size_t mx4_gemm_fwd_bytes(const Mx4Linear& d) { return expanded_bytes(d.w()) + staged_bytes(d, d.in); }
+size_t mx4_gemm_fwd_bytes(const Mx4Linear& d) { return expanded_bytes(d.w()) + staged_bytes(d, d.in) + fwd_part_bytes(d); }
 
 cudaError_t mx4_gemm_fwd(const void* X, const Mx4View& w, const void* bias, const Mx4Linear& d, void* Y, void* ws, int* status,
                          cudaStream_t st) {
   char* wd = (char*)ws;
+  char* xs = wd + expanded_bytes(d.w());
+  float* part = (float*)(xs + staged_bytes(d, d.in));
   StageJob sj;
-  const Operand a = staged(X, d, d.in, wd + expanded_bytes(d.w()), &sj);
-  const cudaError_t e = prepare(d, BiasJob{}, expand_job(w, wd), ExpandJob{}, sj, st);
+  const Operand a = staged(X, d, d.in, xs, &sj);
+  cudaError_t e = prepare(d, BiasJob{}, expand_job(w, wd), ExpandJob{}, sj, st);
   if (e != cudaSuccess) return e;
-  const Result r{Y, d.rows, d.out, d.nb, (int64_t)d.nb * d.out, d.out};
-  const Plan p = plan_for(d.rows, d.out, d.nb, (d.in + 63) / 64 * parts_of(d.dtype), false);
-  return d.dtype == MONARCH_BF16 ? gemm<false, false, __nv_bfloat16>(a, expanded(wd, d.w()), r, bias, d.nb, d.in, 1, p, status, st)
-                                 : gemm<false, false, float>(a, expanded(wd, d.w()), r, bias, d.nb, d.in, 3, p, status, st);
+  const int64_t width = (int64_t)d.nb * d.out, results = d.rows * width;
+  const Plan p = fwd_plan(d);
+  e = product<false, false>(a, expanded(wd, d.w()), Result{Y, d.rows, d.out, d.nb, width, d.out, 0}, bias, d, d.in, p, part, results, status, st);
+  if (e != cudaSuccess || p.nsplit == 1) return e;
+  return sum(d, SumJob{part, results, p.nsplit, bias, width, nullptr, 0, 0}, Y, nullptr, st);
 }
 
 size_t mx4_gemm_bwd_bytes(const Mx4Linear& d) { return bwd_layout(d).total; }
@@ -779,53 +818,41 @@ cudaError_t mx4_gemm_bwd(const void* dY, const Mx4View& x, const Mx4View& w, con
                          void* ws, int* status, cudaStream_t st) {
   const BwdWs l = bwd_layout(d);
   char* base = (char*)ws;
-  const bool bf = d.dtype == MONARCH_BF16;
-  const int parts = parts_of(d.dtype);
-  const int64_t n_out = (int64_t)d.nb * d.out;
+  float* part = (float*)(base + l.part);
+  const int64_t n_in = (int64_t)d.nb * d.in, n_out = (int64_t)d.nb * d.out;
   StageJob sj;
   const Operand a = staged(dY, d, d.out, base + l.dy, &sj);
   if (dX == nullptr && dW == nullptr) sj.blocks = 0;
   BiasJob bj = {};
   if (dbias != nullptr) {
-    const int w16 = n_out * (bf ? 2 : 4) % 16 == 0 ? (bf ? 8 : 4) : 1;  // columns a lane
-    bj = BiasJob{dY, (float*)(base + l.bias), dbias, d.rows, n_out, (int)((n_out + 32 * w16 - 1) / (32 * w16)), bias_parts(d), 0};
+    const int es = d.dtype == MONARCH_BF16 ? 2 : 4, lane = n_out * es % 16 == 0 ? 16 / es : 1;  // columns a lane
+    bj = BiasJob{dY, (float*)(base + l.bias), dbias, d.rows, n_out, (int)((n_out + 32 * lane - 1) / (32 * lane)), bias_parts(d), 0};
     bj.blocks = bj.nparts * bj.cgroups;
   }
   cudaError_t e = prepare(d, bj, dX != nullptr ? expand_job(w, base + l.w) : ExpandJob{}, dW != nullptr ? expand_job(x, base + l.x) : ExpandJob{},
                           sj, st);
   if (e != cudaSuccess) return e;
+  SumJob sums = {};
   if (dX != nullptr) {
-    const Result r{dX, d.rows, d.in, d.nb, (int64_t)d.nb * d.in, d.in};
-    const Plan p = plan_for(d.rows, d.in, d.nb, (d.out + 63) / 64 * parts, false);
-    e = bf ? gemm<false, true, __nv_bfloat16>(a, expanded(base + l.w, d.w()), r, nullptr, d.nb, d.out, 1, p, status, st)
-           : gemm<false, true, float>(a, expanded(base + l.w, d.w()), r, nullptr, d.nb, d.out, 3, p, status, st);
+    const Plan p = dx_plan(d);
+    e = product<false, true>(a, expanded(base + l.w, d.w()), Result{dX, d.rows, d.in, d.nb, n_in, d.in, 0}, nullptr, d, d.out, p, part,
+                             d.rows * n_in, status, st);
+    if (e == cudaSuccess && p.nsplit > 1) e = sum(d, SumJob{part, d.rows * n_in, p.nsplit, nullptr, 1, nullptr, 0, 0}, dX, nullptr, st);
     if (e != cudaSuccess) return e;
   }
-  float* part = nullptr;
-  int64_t n = 0;
-  int nsplit = 0;
   if (dW != nullptr) {
     const Plan p = dw_plan(d);
-    const Operand ak = rows_as_k(a, d, d.out), b = expanded(base + l.x, d.x());
-    if (p.nsplit > 1) {
-      part = (float*)(base + l.part);
-      n = n_out * d.in;
-      nsplit = p.nsplit;
-      const Result r{part, d.out, d.in, (int64_t)d.nb * p.nsplit, d.in, (int64_t)d.out * d.in};
-      e = gemm<true, true, float>(ak, b, r, nullptr, d.nb, d.rows, parts, p, status, st);
-    } else {
-      const Result r{dW, d.out, d.in, d.nb, d.in, (int64_t)d.out * d.in};
-      e = bf ? gemm<true, true, __nv_bfloat16>(ak, b, r, nullptr, d.nb, d.rows, 1, p, status, st)
-             : gemm<true, true, float>(ak, b, r, nullptr, d.nb, d.rows, 3, p, status, st);
-    }
+    e = product<true, true>(rows_as_k(a, d, d.out), expanded(base + l.x, d.x()), Result{dW, d.out, d.in, d.nb, d.in, (int64_t)d.out * d.in, 0},
+                            nullptr, d, d.rows, p, part, n_out * d.in, status, st);
     if (e != cudaSuccess) return e;
+    if (p.nsplit > 1) sums = SumJob{part, n_out * d.in, p.nsplit, nullptr, 1, nullptr, 0, 0};
   }
-  const int64_t cols = dbias != nullptr && bj.nparts > 1 ? n_out : 0;
-  if (n + cols == 0) return cudaSuccess;
-  return bf ? launch_kernel(mx4_sum_kernel<__nv_bfloat16>, dim3(blocks_for(n + cols)), dim3(256), 0, st, true, (const float*)part, n, nsplit,
-                            (__nv_bfloat16*)dW, (const float*)bj.part, cols, bj.nparts, (__nv_bfloat16*)dbias)
-            : launch_kernel(mx4_sum_kernel<float>, dim3(blocks_for(n + cols)), dim3(256), 0, st, true, (const float*)part, n, nsplit,
-                            (float*)dW, (const float*)bj.part, cols, bj.nparts, (float*)dbias);
+  if (dbias != nullptr && bj.nparts > 1) {
+    sums.bpart = bj.part;
+    sums.cols = n_out;
+    sums.nparts = bj.nparts;
+  }
+  return sum(d, sums, dW, dbias, st);
 }
 
 }  // namespace monarch

@@ -374,9 +374,12 @@ cudaError_t launch_token(const void* X, const Mx4View& w, const void* bias, int6
 template <typename TX, int PARTS, typename TY, bool VEC, int NT>
 cudaError_t launch_batch(const void* X, const Mx4View& w, const void* bias, int64_t rows, const Mx4Out& o, void* Y, bool w_early,
                          cudaStream_t st) {
-  const int shares = shares_for(w);
   const int64_t mtiles = (w.s.rows + 15) / 16;
   const int per = (int)(mtiles < kWarps ? mtiles : kWarps);
+  // only as many shares as it takes to give every SM a CTA: each of them costs a start and a join
+  const int64_t ctas = (mtiles + per - 1) / per * w.s.nblocks * ((rows + 8 * NT - 1) / (8 * NT));
+  int shares = 1;
+  while (shares < 8 && shares * 2 <= w.s.katoms() && ctas * shares < num_sms()) shares *= 2;
   const size_t inputs = (size_t)PARTS * 8 * NT * kAhead * 256, sums = (size_t)per * 8 * NT * kSumPitch * 4;
   const size_t smem = inputs > sums ? inputs : sums;
   cudaError_t e = ensure_smem_attr((const void*)mx4_batch_kernel<TX, PARTS, TY, VEC, NT>, smem);

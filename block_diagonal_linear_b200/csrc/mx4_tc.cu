@@ -348,18 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::bulk_wait_read_all();
         }
         __syncwarp();
-        const uint32_t base = slab_s + sbuf * kSlab + lane * 128;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const uint32_t at = base + (((uint32_t)q ^ (uint32_t)(lane & 7)) << 4);
-          if (sizeof(T) == 2)
-            ptx::st_shared_v4(at, ptx::pack_bf16x2(__uint_as_float(v[(8 * q + 0) % CC]), __uint_as_float(v[(8 * q + 1) % CC])),
-                              ptx::pack_bf16x2(__uint_as_float(v[(8 * q + 2) % CC]), __uint_as_float(v[(8 * q + 3) % CC])),
-                              ptx::pack_bf16x2(__uint_as_float(v[(8 * q + 4) % CC]), __uint_as_float(v[(8 * q + 5) % CC])),
-                              ptx::pack_bf16x2(__uint_as_float(v[(8 * q + 6) % CC]), __uint_as_float(v[(8 * q + 7) % CC])));
-          else
-            ptx::st_shared_v4(at, v[(4 * q) % CC], v[(4 * q + 1) % CC], v[(4 * q + 2) % CC], v[(4 * q + 3) % CC]);
-        }
+        mx4::slab_write<T, CC>(slab_s + sbuf * kSlab, lane, v);
         if (TMA_OUT) {
           ptx::fence_proxy_async_smem();
           __syncwarp();
@@ -368,20 +357,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::bulk_commit_group();
           }
         } else {
-          // rows whose pitch is no multiple of 16 bytes: lanes along the columns
+          // rows whose pitch is no multiple of 16 bytes
           __syncwarp();
-          const int cols = job.out - n0 - ch * CC;
-          T* dst = Y + m0 * pitch + (int64_t)c.b * job.out + n0 + ch * CC;
-#pragma unroll 4
-          for (int rr = 0; rr < 32; ++rr) {
-            if (m0 + rr >= job.rows) break;
-            const uint8_t* src = slab + sbuf * kSlab + rr * 128;
-#pragma unroll
-            for (int e = 0; e < CC / 32; ++e) {
-              const int col = e * 32 + lane, byte = col * (int)sizeof(T);
-              if (col < cols) dst[rr * pitch + col] = *(const T*)(src + (((byte >> 4) ^ (rr & 7)) << 4) + (byte & 15));
-            }
-          }
+          mx4::slab_store<T, CC>(slab + sbuf * kSlab, lane, Y + m0 * pitch + (int64_t)c.b * job.out + n0 + ch * CC, pitch,
+                                 (int)min((int64_t)32, job.rows - m0), job.out - n0 - ch * CC);
         }
       }
     }
@@ -479,18 +458,32 @@ cudaError_t launch_out(const Mx4View& x, const Mx4View& w, const void* bias, con
 template <typename T>
 cudaError_t launch_type(const Mx4View& x, const Mx4View& w, const void* bias, const Mx4Linear& d, void* Y, int* status,
                         cudaStream_t st) {
-  // a pair's two CTAs wait for each other once a tile, which only a long K hides: 8192 rows -> 4096 take
-  // 19.7 us on pairs and 14.1 on single CTAs with 256 inputs, 22.2 and 17.7 with 512, 27.1 and 26.6 with 1024,
-  // 60.6 and 75 with 4096
-  if (d.in >= 1024 && d.out > 128 && (d.rows + 255) / 256 * d.nb * ((d.out + 255) / 256) >= num_sms() / 2)
-    return launch_out<256, true, T>(x, w, bias, d, Y, status, st);
-  // the widest tile that the outputs fill, halved while there are fewer tiles than SMs
-  int bn = d.out > 128 ? 256 : d.out > 64 ? 128 : 64;
-  while (bn > 64 && x.s.ratoms() * d.nb * ((d.out + bn - 1) / bn) < num_sms()) bn /= 2;
-  switch (bn) {
-    case 64: return launch_out<64, false, T>(x, w, bias, d, Y, status, st);
-    case 128: return launch_out<128, false, T>(x, w, bias, d, Y, status, st);
-    default: return launch_out<256, false, T>(x, w, bias, d, Y, status, st);
+  // The tile whose rounds over the SMs take the least time: a tile costs a stage's share of the way from
+  // L2 for every 256 inputs, and its epilogue.  Microseconds from 8192 rows -> 4096 (256 x 256 pairs,
+  // 128 x 256 single): 19.7 and 14.1 with 256 inputs, 22.2 and 17.7 with 512, 27.1 and 26.6 with 1024, 60.6 and 75 with
+  // 4096; a pair's two CTAs wait for each other once a tile, which only a long K hides.
+  struct Tile {
+    int bm, bn;
+    double stage, fixed;
+  };
+  const Tile tiles[4] = {{256, 256, 0.46, 2.3}, {128, 256, 0.62, 1.3}, {128, 128, 0.42, 1.0}, {128, 64, 0.30, 0.8}};
+  int best = 0;
+  double least = 1e30;
+  for (int i = 0; i < 4; ++i) {
+    if (i < 3 && d.out <= tiles[i].bn / 2) continue;  // half of it or more would be empty
+    const int64_t units = (d.rows + tiles[i].bm - 1) / tiles[i].bm * d.nb * ((d.out + tiles[i].bn - 1) / tiles[i].bn);
+    const int64_t slots = i == 0 ? num_sms() / 2 : num_sms();
+    const double t = (double)((units + slots - 1) / slots) * ((x.s.cols + 255) / 256 * tiles[i].stage + tiles[i].fixed);
+    if (t < least) {
+      least = t;
+      best = i;
+    }
+  }
+  switch (best) {
+    case 0: return launch_out<256, true, T>(x, w, bias, d, Y, status, st);
+    case 1: return launch_out<256, false, T>(x, w, bias, d, Y, status, st);
+    case 2: return launch_out<128, false, T>(x, w, bias, d, Y, status, st);
+    default: return launch_out<64, false, T>(x, w, bias, d, Y, status, st);
   }
 }
 
