@@ -102,6 +102,66 @@ __device__ __forceinline__ void values8(uint32_t w, uint32_t byte, uint32_t (&v)
   v[3] = __byte_perm(p[2], p[3], 0x7632);
 }
 
+// Words o .. o + 4 of eight (o in 0 .. 3).
+__device__ __forceinline__ void pick5(const uint32_t (&w)[8], int o, uint32_t (&r)[5]) {
+  uint32_t t[6];
+#pragma unroll
+  for (int i = 0; i < 6; ++i) t[i] = (o & 2) ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) r[i] = (o & 1) ? t[i + 1] : t[i];
+}
+// Eight values from an address of any alignment, n of them (<= 0: none) inside the row, zeros behind it: the
+// aligned 16-byte words that hold them, shifted into place.  end: the end of the tensor (a tensor begins
+// on 16 bytes), behind which no word may reach.  x: bf16 pairs or fp32 bits.
+__device__ __forceinline__ void load8_any(const __nv_bfloat16* p, int n, const __nv_bfloat16* end, uint32_t (&x)[8]) {
+  uint32_t r[4] = {};
+  if (n > 0) {
+    const uintptr_t a = (uintptr_t)p & ~(uintptr_t)15;
+    const int at = (int)((uintptr_t)p & 15), last = at + 2 * min(n, 8);  // bytes from a
+    if (a + (last > 16 ? 32 : 16) <= (uintptr_t)end) {
+      const uint4 u = *(const uint4*)a, v = last > 16 ? *(const uint4*)(a + 16) : make_uint4(0, 0, 0, 0);
+      const uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+      uint32_t t[5];
+      pick5(w, at >> 2, t);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r[i] = __byte_perm(t[i], t[i + 1], (at & 2) ? 0x5432u : 0x3210u);
+      if (n < 8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] &= (2 * i < n ? 0xffffu : 0u) | (2 * i + 1 < n ? 0xffff0000u : 0u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < n) r[i / 2] |= (uint32_t)*(const uint16_t*)(p + i) << (16 * (i & 1));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = r[i];
+}
+__device__ __forceinline__ void load8_any(const float* p, int n, const float* end, uint32_t (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = 0;
+  if (n <= 0) return;
+  const uintptr_t a = (uintptr_t)p & ~(uintptr_t)15;
+  const int at = (int)((uintptr_t)p & 15) >> 2;
+  if (n >= 8 && a + 48 <= (uintptr_t)end) {
+    const uint4 u = *(const uint4*)a, v = *(const uint4*)(a + 16), q = at ? *(const uint4*)(a + 32) : make_uint4(0, 0, 0, 0);
+    const uint32_t w0[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w}, w1[8] = {v.x, v.y, v.z, v.w, q.x, q.y, q.z, q.w};
+    uint32_t t0[5], t1[5];
+    pick5(w0, at, t0);
+    pick5(w1, at, t1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = t0[i];
+      x[4 + i] = t1[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) x[i] = __float_as_uint(p[i]);
+  }
+}
+
 // A warp's 32 rows x 128 bytes of results: written to shared memory as 128-byte swizzled lines (one row a
 // lane; the layout that a TMA store of 32 rows takes), and from there to rows of any alignment.
 template <typename T, int CC>

@@ -395,35 +395,40 @@ struct StageJob {
   int cols, pitch;
   int64_t blocks;
 };
-constexpr int kStagePer = 8;  // pairs of values a thread
+constexpr int kStagePer = 2;  // times 8 values a thread
 template <typename T>
-__device__ __forceinline__ void stage_pairs(const StageJob& j, int64_t blk) {
+__device__ __forceinline__ void stage_rows(const StageJob& j, int64_t blk) {
   constexpr int PARTS = sizeof(T) == 2 ? 1 : 3;
-  const uint32_t words = j.pitch / 2;
+  const uint32_t words = j.pitch / 8;  // 16-byte words of a row
   const int64_t first = blk * (256 * kStagePer), total = j.nrb * words;
   const T* X = (const T*)j.X;
-  float x[kStagePer][2];
-  int64_t row[kStagePer];
-  int c[kStagePer];
+  uint32_t x[kStagePer][8];
+  int64_t to[kStagePer];
 #pragma unroll
   for (int u = 0; u < kStagePer; ++u) {
-    const int64_t e = first + u * 256 + threadIdx.x;
-    row[u] = e / words;
-    c[u] = (int)(e - row[u] * words) * 2;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) x[u][i] = e < total && c[u] + i < j.cols ? mx4::load(X + row[u] * j.cols + c[u] + i) : 0.f;
+    const int64_t e = first + u * 256 + threadIdx.x, row = e / words;
+    const int c = (int)(e - row * words) * 8;
+    to[u] = row * PARTS * j.pitch + c;
+    mx4::load8_any(X + row * j.cols + c, e < total ? j.cols - c : 0, X + j.nrb * j.cols, x[u]);
   }
 #pragma unroll
   for (int u = 0; u < kStagePer; ++u) {
     if (first + u * 256 + threadIdx.x >= total) break;
-    uint32_t* dst = (uint32_t*)(j.out + row[u] * PARTS * j.pitch + c[u]);
+    uint4* dst = (uint4*)(j.out + to[u]);
+    if (PARTS == 1) {
+      *dst = make_uint4(x[u][0], x[u][1], x[u][2], x[u][3]);
+    } else {
 #pragma unroll
-    for (int p = PARTS - 1; p >= 0; --p) {
-      dst[p * words] = (__float_as_uint(x[u][0]) >> 16) | (__float_as_uint(x[u][1]) & 0xffff0000u);
+      for (int p = PARTS - 1; p >= 0; --p) {
+        uint32_t w[4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t top = __float_as_uint(x[u][i]) & 0xffff0000u;
-        x[u][i] = (top & 0x7f800000u) == 0x7f800000u ? 0.f : x[u][i] - __uint_as_float(top);
+        for (int i = 0; i < 4; ++i) w[i] = __byte_perm(x[u][2 * i], x[u][2 * i + 1], 0x7632);
+        dst[p * words] = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t top = x[u][i] & 0xffff0000u;
+          x[u][i] = (top & 0x7f800000u) == 0x7f800000u ? 0u : __float_as_uint(__uint_as_float(x[u][i]) - __uint_as_float(top));
+        }
       }
     }
   }
@@ -495,7 +500,7 @@ __device__ __forceinline__ void bias_part(const BiasJob& j, int64_t blk, float (
 }
 
 template <typename T>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 4)  // the most demanding job must not cost the others their occupancy
     mx4_prepare_kernel(const __grid_constant__ BiasJob bias, const __grid_constant__ ExpandJob e0, const __grid_constant__ ExpandJob e1,
                        const __grid_constant__ StageJob stage) {
   __shared__ float sums[8][32 * 8];
@@ -511,7 +516,7 @@ __global__ void __launch_bounds__(256)
   }
   blk -= bias.blocks;
   if (blk < stage.blocks) {
-    stage_pairs<T>(stage, blk);
+    stage_rows<T>(stage, blk);
     return;
   }
   blk -= stage.blocks;
@@ -622,7 +627,7 @@ Plan plan_for(int64_t m, int n, int nb, int nk) {
       const int per = (nk + want - 1) / want, ns = (nk + per - 1) / per;
       const int64_t rounds = (tiles * ns + slots - 1) / slots;
       double t = (double)rounds * (per * (pair ? 0.40 : 0.33) + (pair ? 2.0 : 1.2));
-      if (ns > 1) t += 2.5 + (double)m * n * nb * 4 * (ns + 1) / 5e6;
+      if (ns > 1) t += 4.0 + (double)m * n * nb * 4 * (ns + 1) / 4e6;
       if (t < least) {
         least = t;
         best = Plan{pair != 0, ns, per};
@@ -729,7 +734,7 @@ Operand staged(const void* X, const Mx4Linear& d, int blk, void* ws, StageJob* j
   if (direct(d.dtype, blk)) return Operand{X, blk, d.rows, d.nb, (int64_t)d.nb * blk, blk};
   const int pitch = up(blk, 64);
   *job = StageJob{X, (__nv_bfloat16*)ws, d.rows * d.nb, blk, pitch, 0};
-  job->blocks = (job->nrb * (pitch / 2) + 256 * kStagePer - 1) / (256 * kStagePer);
+  job->blocks = (job->nrb * (pitch / 8) + 256 * kStagePer - 1) / (256 * kStagePer);
   return Operand{ws, (int64_t)parts * pitch, d.rows, d.nb, (int64_t)d.nb * parts * pitch, (int64_t)parts * pitch};
 }
 int64_t bias_parts(const Mx4Linear& d) { return (d.rows + kBiasRows - 1) / kBiasRows; }

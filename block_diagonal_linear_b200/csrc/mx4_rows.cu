@@ -37,30 +37,25 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Eight neighbouring inputs of one token in fp32 bits or bf16 pairs; zero behind the end.
+// Eight neighbouring inputs of one token in fp32 bits or bf16 pairs, n of them (<= 0: none) inside the row;
+// zero behind its end.  VEC: rows are whole numbers of 16 bytes; end: of X.
 template <bool VEC>
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, int n, uint32_t (&x)[8]) {
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, int n, const __nv_bfloat16* end, uint32_t (&x)[8]) {
   if (VEC) {
     const uint4 u = n > 0 ? *(const uint4*)p : make_uint4(0, 0, 0, 0);
     x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
   } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t lo = 2 * i < n ? *(const uint16_t*)(p + 2 * i) : 0u;
-      const uint32_t hi = 2 * i + 1 < n ? *(const uint16_t*)(p + 2 * i + 1) : 0u;
-      x[i] = lo | (hi << 16);
-    }
+    mx4::load8_any(p, n, end, x);
   }
 }
 template <bool VEC>
-__device__ __forceinline__ void load8(const float* p, int n, uint32_t (&x)[8]) {
+__device__ __forceinline__ void load8(const float* p, int n, const float* end, uint32_t (&x)[8]) {
   if (VEC) {
     const uint4 u = n > 0 ? *(const uint4*)p : make_uint4(0, 0, 0, 0), w = n > 4 ? *(const uint4*)(p + 4) : make_uint4(0, 0, 0, 0);
     x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
     x[4] = w.x; x[5] = w.y; x[6] = w.z; x[7] = w.w;
   } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = i < n ? *(const uint32_t*)(p + i) : 0u;
+    mx4::load8_any(p, n, end, x);
   }
 }
 
@@ -179,6 +174,8 @@ __global__ void __launch_bounds__(kWarps * 32)
   const CodeRows cr(w, b, (tile0 + mw) * 16 + g, t);
   const __nv_bfloat16* p = X + (int64_t)g * w.s.nblocks * w.s.cols + (int64_t)b * w.s.cols + t * 32;
 
+  const __nv_bfloat16* end = X + rows * w.s.nblocks * w.s.cols;
+
   float acc[4] = {};
   Codes c[kAhead];
   // weights that no kernel of this stream is still writing may be asked for ahead of the wait
@@ -199,7 +196,7 @@ __global__ void __launch_bounds__(kWarps * 32)
       if (ka >= cr.katoms) break;
       uint32_t x[4][8], a0[16], a1[16];
 #pragma unroll
-      for (int v = 0; v < 4; ++v) load8<VEC>(p + ka * 128 + 8 * v, g < rows ? w.s.cols - ka * 128 - t * 32 - 8 * v : 0, x[v]);
+      for (int v = 0; v < 4; ++v) load8<VEC>(p + ka * 128 + 8 * v, g < rows ? w.s.cols - ka * 128 - t * 32 - 8 * v : 0, end, x[v]);
       values(c[i], t, a0, a1);
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
@@ -235,7 +232,7 @@ constexpr int kSumPitch = 20;  // 16 outputs of a token, padded: 16-byte reads, 
 
 // All 8 warps bring the inputs in; the first `per` compute.
 template <typename TX, int PARTS, typename TY, bool VEC, int NT>
-__global__ void __launch_bounds__(kWarps * 32, PARTS > 1 && NT == 8 ? 1 : 2)  // two CTAs an SM where shared memory holds them
+__global__ void __launch_bounds__(kWarps * 32, 2)
     mx4_batch_kernel(const TX* X, Mx4View w, int64_t rows, Mx4Out o, const TY* bias, TY* Y, int shares, int per, bool w_early) {
   constexpr int U = sizeof(TX) == 2 ? 8 : 4;  // chunks of 8 inputs a thread asks for before it stores the first
   extern __shared__ uint4 xs[];  // [PARTS][8 * NT][kAhead * 16]
@@ -279,7 +276,8 @@ __global__ void __launch_bounds__(kWarps * 32, PARTS > 1 && NT == 8 ? 1 : 2)  //
         const int e = e0 + u * kWarps * 32;
         token[u] = e / (n * 16);
         ch[u] = e - token[u] * (n * 16);
-        load8<VEC>(xb + token[u] * pitch + ka0 * 128 + ch[u] * 8, token[u] < tokens ? w.s.cols - ka0 * 128 - ch[u] * 8 : 0, x[u]);
+        load8<VEC>(xb + token[u] * pitch + ka0 * 128 + ch[u] * 8, token[u] < tokens ? w.s.cols - ka0 * 128 - ch[u] * 8 : 0,
+                   X + rows * pitch, x[u]);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -411,9 +409,12 @@ cudaError_t launch_vec(const void* X, const Mx4View& w, const void* bias, int64_
     else
       return launch_batch<TX, PARTS, TY, VEC, 1>(X, w, bias, rows, o, Y, w_early, st);
   }
-  return rows <= 16   ? launch_batch<TX, PARTS, TY, VEC, 2>(X, w, bias, rows, o, Y, w_early, st)
-         : rows <= 32 ? launch_batch<TX, PARTS, TY, VEC, 4>(X, w, bias, rows, o, Y, w_early, st)
-                      : launch_batch<TX, PARTS, TY, VEC, 8>(X, w, bias, rows, o, Y, w_early, st);
+  if (rows <= 16) return launch_batch<TX, PARTS, TY, VEC, 2>(X, w, bias, rows, o, Y, w_early, st);
+  if constexpr (PARTS == 1) {
+    if (rows > 32) return launch_batch<TX, PARTS, TY, VEC, 8>(X, w, bias, rows, o, Y, w_early, st);
+  }
+  // several parts of 64 tokens would leave an SM one CTA: 32 tokens a pass
+  return launch_batch<TX, PARTS, TY, VEC, 4>(X, w, bias, rows, o, Y, w_early, st);
 }
 
 template <typename TX, int PARTS, typename TY>

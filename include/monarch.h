@@ -382,8 +382,8 @@ typedef struct {
 } monarch_mx4_linear_dims;
 
 /* Workspace of monarch_mx4_linear_wfwd and of monarch_mx4_linear_bwd, 256-byte aligned (0: may be NULL; 0
- * if ld is bad).  It holds the MX4 operand's values in bf16 beyond 64 rows, plain operands whose rows TMA
- * cannot address, and partial sums. */
+ * if ld is bad).  It holds the MX4 operands' values in bf16 (forward: beyond 64 bf16 or 32 fp32 rows), plain
+ * operands whose rows TMA cannot address, and partial sums. */
 MONARCH_API size_t monarch_mx4_linear_wfwd_workspace_bytes(const monarch_mx4_linear_dims* ld);
 MONARCH_API size_t monarch_mx4_linear_bwd_workspace_bytes(const monarch_mx4_linear_dims* ld);
 /* Both operands in MX4. */
