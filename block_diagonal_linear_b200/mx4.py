@@ -34,7 +34,7 @@ class Mx4:
     ``dtype`` is that tensor's type ("bf16" / "f32")."""
 
     # _hold: what keeps the memory alive; _pc, _ps: addresses of codes and scales; _index: their device;
-    # _layers: (rows, has_bias, code) -> dims of a layer with this weight and its workspace bytes
+    # _layers: dims of a layer or map with this weight and its workspace bytes, by the rest of the dims
     __slots__ = ("rows", "nblocks", "cols", "by_block", "code", "_hold", "_sizes", "_pc", "_ps", "_index", "_layers")
 
     def __init__(self, codes, scales, rows: int, nblocks: int, cols: int, by_block: bool, dtype):
@@ -61,6 +61,9 @@ class Mx4:
         q._ps = q._pc + at
         q._index = like.get_device()
         return q
+
+    def _memory(self):
+        return self._hold[0] if isinstance(self._hold, tuple) else self._hold
 
     @property
     def codes(self):
@@ -127,7 +130,7 @@ def _together(device, *qs):
 def _empty(like, shape, dtype, stream):
     """Memory on like's device for work on `stream` (None: that device's current one)."""
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return like.new_empty(shape) if dtype is like.dtype else like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
         return like.new_empty(shape, dtype=dtype)
 
@@ -194,8 +197,7 @@ def mx4_dequantise(q: Mx4, dtype=None, out=None, stream=None):
     code = q.code if dtype is None else dtype_code(dtype)
     dt = _DTYPES[code]
     if out is None:
-        like = q._hold[0] if isinstance(q._hold, tuple) else q._hold
-        out = _empty(like, q.shape, dt, stream)
+        out = _empty(q._memory(), q.shape, dt, stream)
     elif tuple(out.shape) != tuple(q.shape) or out.dtype != dt:
         raise ValueError("out must be %s of shape %s" % (dt, tuple(q.shape)))
     device = _device(out)
@@ -220,15 +222,20 @@ def _expect(t, name, shape, dtype):
         raise ValueError("%s must be %s of shape %s, is %s of shape %s" % (name, dtype, shape, t.dtype, tuple(t.shape)))
 
 
+def _remember(W, key, plan):
+    if len(W._layers) >= 64:  # a serving loop sees few batch sizes; any number must not pile up
+        W._layers.clear()
+    W._layers[key] = plan
+    return plan
+
+
 def _layer(W, rows, has_bias, code):
     """(dims by reference, forward workspace bytes, backward workspace bytes) of a layer with weight W."""
-    plan = W._layers.get((rows, has_bias, code))
+    key = (rows, has_bias, code)
+    plan = W._layers.get(key)
     if plan is None:
-        if len(W._layers) >= 64:  # a serving loop sees few batch sizes; any number must not pile up
-            W._layers.clear()
         d, L = _byref(MonarchMx4LinearDims(rows, W.nblocks, W.cols, W.rows, has_bias, code)), lib()
-        plan = W._layers[(rows, has_bias, code)] = (d, L.monarch_mx4_linear_wfwd_workspace_bytes(d),
-                                                    L.monarch_mx4_linear_bwd_workspace_bytes(d))
+        plan = _remember(W, key, (d, L.monarch_mx4_linear_wfwd_workspace_bytes(d), L.monarch_mx4_linear_bwd_workspace_bytes(d)))
     return plan
 
 
@@ -246,38 +253,41 @@ def mx4_linear_fwd(X, W: Mx4, bias=None, Y=None, dtype=None, workspace=None, str
     X is a plain tensor (rows, nblocks * in_blk), or an Mx4 of one; then Y has `dtype` (default: the type
     X was quantised from)."""
     _weight(W)
-    both = isinstance(X, Mx4)
-    if both:
+    n_out = W.nblocks * W.rows
+    if isinstance(X, Mx4):
         _activations(X, W)
         code = X.code if dtype is None else dtype_code(dtype)
-        rows = X.rows
-    else:
-        code = _code(X, "X")
-        if dtype is not None and dtype_code(dtype) != code:
-            raise ValueError("dtype is X's unless X is an Mx4")
-        rows = X.shape[0]
-        _expect(X, "X", (rows, W.nblocks * W.cols), X.dtype)
-    dt = _DTYPES[code]
-    n_out = W.nblocks * W.rows
-    if bias is not None:
-        _expect(bias, "bias", (n_out,), dt)
-    if Y is None:
-        like = X if not both else X._hold[0] if isinstance(X._hold, tuple) else X._hold
-        Y = _empty(like, (rows, n_out), dt, stream)
-    else:
-        _expect(Y, "Y", (rows, n_out), dt)
-    d, need, _ = _layer(W, rows, bias is not None, code)
-    if both:
+        rows, dt = X.rows, _DTYPES[code]
+        if bias is not None:
+            _expect(bias, "bias", (n_out,), dt)
+        if Y is None:
+            Y = _empty(X._memory(), (rows, n_out), dt, stream)
+        else:
+            _expect(Y, "Y", (rows, n_out), dt)
         device = _device(Y, bias)
         _together(device, W, X)
-        _call("monarch_mx4_linear_fwd", lib().monarch_mx4_linear_fwd, device, stream, X._pc, X._ps, W._pc, W._ps, _p(bias), d,
-              Y.data_ptr())
-    else:
-        device = _device(X, Y, bias, workspace)
-        _together(device, W)
-        workspace, wp, wn = _workspace(workspace, need, X, stream)
-        _call("monarch_mx4_linear_wfwd", lib().monarch_mx4_linear_wfwd, device, stream, X.data_ptr(), W._pc, W._ps, _p(bias), d,
-              Y.data_ptr(), wp, wn)
+        _call("monarch_mx4_linear_fwd", lib().monarch_mx4_linear_fwd, device, stream, X._pc, X._ps, W._pc, W._ps, _p(bias),
+              _layer(W, rows, bias is not None, code)[0], Y.data_ptr())
+        return Y
+    dt = X.dtype
+    code = _code(X, "X")
+    if dtype is not None and dtype_code(dtype) != code:
+        raise ValueError("dtype is X's unless X is an Mx4")
+    rows = X.shape[0]
+    if X.shape != (rows, W.nblocks * W.cols):
+        _expect(X, "X", (rows, W.nblocks * W.cols), dt)
+    if bias is not None:
+        _expect(bias, "bias", (n_out,), dt)
+    if Y is not None:
+        _expect(Y, "Y", (rows, n_out), dt)
+    device = _device(X, bias, Y, workspace)
+    _together(device, W)
+    if Y is None:
+        Y = _empty(X, (rows, n_out), dt, stream)
+    d, need, _ = _layer(W, rows, bias is not None, code)
+    workspace, wp, wn = _workspace(workspace, need, X, stream)
+    _call("monarch_mx4_linear_wfwd", lib().monarch_mx4_linear_wfwd, device, stream, X.data_ptr(), W._pc, W._ps, _p(bias), d,
+          Y.data_ptr(), wp, wn)
     return Y
 
 
@@ -334,15 +344,21 @@ def mx4_fwd(X, R: Mx4, L: Mx4, shape: dict, Y=None, workspace=None, stream=None)
     code = _code(X, "X")
     dt = X.dtype
     rows = X.shape[0]
-    _expect(X, "X", (rows, nb1 * in1), dt)
-    if Y is None:
-        Y = _empty(X, (rows, nb2 * out2), dt, stream)
-    else:
+    if X.shape != (rows, nb1 * in1):
+        _expect(X, "X", (rows, nb1 * in1), dt)
+    if Y is not None:
         _expect(Y, "Y", (rows, nb2 * out2), dt)
-    d = _byref(MonarchDims(rows, nb1, in1, out1, nb2, in2, out2, int(shape.get("out_transpose", 1)), code))
-    lb = lib()
     device = _device(X, Y, workspace)
     _together(device, R, L)
-    workspace, wp, wn = _workspace(workspace, lb.monarch_mx4_fwd_workspace_bytes(d), X, stream)
-    _call("monarch_mx4_fwd", lb.monarch_mx4_fwd, device, stream, X.data_ptr(), R._pc, R._ps, L._pc, L._ps, d, Y.data_ptr(), wp, wn)
+    if Y is None:
+        Y = _empty(X, (rows, nb2 * out2), dt, stream)
+    # R's cache: dims of a map with this factor and its workspace bytes, by what else is in the dims
+    key = (rows, code, nb2, in2, out2, shape.get("out_transpose", 1))
+    plan = R._layers.get(key)
+    if plan is None:
+        d = _byref(MonarchDims(rows, nb1, in1, out1, nb2, in2, out2, int(key[-1]), code))
+        plan = _remember(R, key, (d, lib().monarch_mx4_fwd_workspace_bytes(d)))
+    workspace, wp, wn = _workspace(workspace, plan[1], X, stream)
+    _call("monarch_mx4_fwd", lib().monarch_mx4_fwd, device, stream, X.data_ptr(), R._pc, R._ps, L._pc, L._ps, plan[0], Y.data_ptr(),
+          wp, wn)
     return Y

@@ -255,7 +255,8 @@ def test_extreme_scales():
 MONARCH = [  # (rows, nb1, in1, out1, nb2, in2, out2, out_transpose)
     (1, 4, 256, 256, 4, 256, 1024, 0), (3, 16, 16, 16, 16, 16, 16, 1), (1, 64, 64, 64, 64, 64, 64, 1),
     (32, 32, 32, 32, 32, 32, 32, 1), (33, 16, 48, 48, 48, 16, 64, 1), (7, 4, 250, 250, 4, 250, 1000, 0),
-    (5, 3, 10, 8, 4, 6, 5, 1), (2, 1, 40, 24, 2, 12, 9, 0), (64, 4, 256, 64, 4, 64, 64, 0), (65, 8, 64, 64, 8, 64, 128, 0),
+    (5, 3, 10, 8, 4, 6, 5, 1), (2, 1, 40, 24, 2, 12, 9, 0), (9, 2, 300, 129, 6, 43, 17, 1), (12, 5, 33, 70, 7, 50, 21, 0),
+    (3, 2, 2048, 1100, 2, 1100, 1030, 0), (20, 8, 640, 640, 8, 640, 1024, 1), (64, 4, 256, 64, 4, 64, 64, 0), (65, 8, 64, 64, 8, 64, 128, 0),
     (200, 32, 32, 32, 32, 32, 32, 1), (300, 4, 256, 256, 4, 256, 1024, 0)]
 
 
