@@ -40,6 +40,7 @@ struct GJob {
   int64_t d_b, d_m, d_s;  // D strides (elements) of a block, a row and a split, for the epilogue without TMA
   int nk, parts;       // K stages of one part; parts of A
   int stages_per_split;
+  int beside;          // run beside the kernel that was launched just before (see the kernel)
   int a_chunked, b_chunked;  // inner index M / N: the map is 4-D and both 64-wide chunks are one box
 };
 
@@ -159,7 +160,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (PAIR) ptx::cluster_sync_all();  // both CTAs' barriers exist and TMEM is allocated
   ptx::tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
-  ptx::griddep_wait();
+  // beside: the kernel just before neither writes what this one reads nor touches what it writes, and had
+  // itself waited for all before it when it let this one start; so this one takes the SMs that it leaves
+  // free, and waits for it at the end (for the kernels after this one, which see both as done)
+  if (!job.beside) ptx::griddep_wait();
   ptx::griddep_launch_dependents();
 
   if (warp == 0) {
@@ -343,6 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     else
       ptx::tmem_dealloc(tmem, C::TMEM_COLS);
   }
+  if (job.beside) ptx::griddep_wait();
 }
 
 // ---------------------------------------------------------------- operand preparation
@@ -526,34 +531,29 @@ __global__ void __launch_bounds__(256, 4)  // the most demanding job must not co
     expand_tile(e1, blk - e0.blocks);
 }
 
-// What is left to add at the end, parts in order: out[e] over nsplit parts of n values (+ bias[e % width]),
-// dbias[c] over nparts parts of cols.
+// What is left to add at the end, parts in order: out[e] over nsplit parts of n values (+ bias[e % width]).
 struct SumJob {
   const float* part;
-  int64_t n;
-  int nsplit;
+  void* out;
+  int64_t n, nsplit;
   const void* bias;
   int64_t width;
-  const float* bpart;
-  int64_t cols, nparts;
 };
 template <typename T>
-__global__ void __launch_bounds__(256) mx4_sum_kernel(const __grid_constant__ SumJob j, T* __restrict__ out, T* __restrict__ dbias) {
+__global__ void __launch_bounds__(256)
+    mx4_sum_kernel(const __grid_constant__ SumJob j0, const __grid_constant__ SumJob j1, const __grid_constant__ SumJob j2) {
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
-  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < j.n + j.cols; e += (int64_t)gridDim.x * 256) {
-    const bool b = e >= j.n;
-    const float* p = b ? j.bpart + (e - j.n) : j.part + e;
-    const int64_t step = b ? j.cols : j.n, m = b ? j.nparts : j.nsplit;
+  const int64_t total = j0.n + j1.n + j2.n;
+  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += (int64_t)gridDim.x * 256) {
+    const bool second = e >= j0.n, third = e >= j0.n + j1.n;
+    const SumJob& j = third ? j2 : second ? j1 : j0;
+    const int64_t i = e - (third ? j0.n + j1.n : second ? j0.n : 0);
     float acc = 0.f;
 #pragma unroll 8
-    for (int64_t s = 0; s < m; ++s) acc += p[s * step];
-    if (b) {
-      st_from_f32(dbias + (e - j.n), acc);
-    } else {
-      if (j.bias != nullptr) acc += mx4::load((const T*)j.bias + e % j.width);
-      st_from_f32(out + e, acc);
-    }
+    for (int64_t s = 0; s < j.nsplit; ++s) acc += j.part[s * j.n + i];
+    if (j.bias != nullptr) acc += mx4::load((const T*)j.bias + i % j.width);
+    st_from_f32((T*)j.out + i, acc);
   }
 }
 
@@ -682,8 +682,9 @@ cudaError_t launch(const Operand& a, const Operand& b, const Result& d, const vo
 
 template <bool A_MN, bool B_MN, typename T>
 cudaError_t gemm(const Operand& a, const Operand& b, const Result& d, const void* bias, int nb, int64_t k, int parts, const Plan& p,
-                 int* status, cudaStream_t st) {
+                 bool beside, int* status, cudaStream_t st) {
   GJob j = {};
+  j.beside = beside;
   j.nb = nb;
   j.nsplit = p.nsplit;
   j.m = d.m;
@@ -763,36 +764,36 @@ Operand expanded(const void* p, const Mx4Shape& s) {
 // One product into `out` (results in the order of `r`), or into fp32 parts when K is split.
 template <bool A_MN, bool B_MN>
 cudaError_t product(const Operand& a, const Operand& b, Result r, const void* bias, const Mx4Linear& d, int64_t k, const Plan& p,
-                    float* part, int64_t results, int* status, cudaStream_t st) {
+                    float* part, int64_t results, bool beside, int* status, cudaStream_t st) {
   const int parts = parts_of(d.dtype);
   r.d_s = results;
   if (p.nsplit > 1) {
     r.p = part;
-    return gemm<A_MN, B_MN, float>(a, b, r, nullptr, d.nb, k, parts, p, status, st);
+    return gemm<A_MN, B_MN, float>(a, b, r, nullptr, d.nb, k, parts, p, beside, status, st);
   }
   r.d_s = up64(results);  // one part: any stride that a tensor map takes
-  return d.dtype == MONARCH_BF16 ? gemm<A_MN, B_MN, __nv_bfloat16>(a, b, r, bias, d.nb, k, parts, p, status, st)
-                                 : gemm<A_MN, B_MN, float>(a, b, r, bias, d.nb, k, parts, p, status, st);
+  return d.dtype == MONARCH_BF16 ? gemm<A_MN, B_MN, __nv_bfloat16>(a, b, r, bias, d.nb, k, parts, p, beside, status, st)
+                                 : gemm<A_MN, B_MN, float>(a, b, r, bias, d.nb, k, parts, p, beside, status, st);
 }
-cudaError_t sum(const Mx4Linear& d, const SumJob& j, void* out, void* dbias, cudaStream_t st) {
-  if (j.n + j.cols == 0) return cudaSuccess;
-  const dim3 grid(blocks_for(j.n + j.cols));
-  return d.dtype == MONARCH_BF16
-             ? launch_kernel(mx4_sum_kernel<__nv_bfloat16>, grid, dim3(256), 0, st, true, j, (__nv_bfloat16*)out, (__nv_bfloat16*)dbias)
-             : launch_kernel(mx4_sum_kernel<float>, grid, dim3(256), 0, st, true, j, (float*)out, (float*)dbias);
+cudaError_t sum(int dtype, const SumJob& j0, const SumJob& j1, const SumJob& j2, cudaStream_t st) {
+  const int64_t n = j0.n + j1.n + j2.n;
+  if (n == 0) return cudaSuccess;
+  return dtype == MONARCH_BF16 ? launch_kernel(mx4_sum_kernel<__nv_bfloat16>, dim3(blocks_for(n)), dim3(256), 0, st, true, j0, j1, j2)
+                               : launch_kernel(mx4_sum_kernel<float>, dim3(blocks_for(n)), dim3(256), 0, st, true, j0, j1, j2);
 }
 
-// Scratch: the operands in bf16, split sums, parts of dbias.  dX's split sums are joined before dW's are made.
+// Scratch: the operands in bf16, split sums of dX and of dW, parts of dbias.
 struct BwdWs {
-  size_t w, x, dy, part, bias, total;
+  size_t w, x, dy, part_x, part_w, bias, total;
 };
 BwdWs bwd_layout(const Mx4Linear& d) {
   BwdWs l;
   l.w = 0;
   l.x = l.w + expanded_bytes(d.w());
   l.dy = l.x + expanded_bytes(d.x());
-  l.part = l.dy + staged_bytes(d, d.out);
-  l.bias = l.part + std::max(dx_part_bytes(d), dw_part_bytes(d));
+  l.part_x = l.dy + staged_bytes(d, d.out);
+  l.part_w = l.part_x + dx_part_bytes(d);
+  l.bias = l.part_w + dw_part_bytes(d);
   l.total = l.bias + bias_part_bytes(d);
   return l;
 }
@@ -812,9 +813,10 @@ cudaError_t mx4_gemm_fwd(const void* X, const Mx4View& w, const void* bias, cons
   if (e != cudaSuccess) return e;
   const int64_t width = (int64_t)d.nb * d.out, results = d.rows * width;
   const Plan p = fwd_plan(d);
-  e = product<false, false>(a, expanded(wd, d.w()), Result{Y, d.rows, d.out, d.nb, width, d.out, 0}, bias, d, d.in, p, part, results, status, st);
+  e = product<false, false>(a, expanded(wd, d.w()), Result{Y, d.rows, d.out, d.nb, width, d.out, 0}, bias, d, d.in, p, part, results,
+                            false, status, st);
   if (e != cudaSuccess || p.nsplit == 1) return e;
-  return sum(d, SumJob{part, results, p.nsplit, bias, width, nullptr, 0, 0}, Y, nullptr, st);
+  return sum(d.dtype, SumJob{part, Y, results, p.nsplit, bias, width}, SumJob{}, SumJob{}, st);
 }
 
 size_t mx4_gemm_bwd_bytes(const Mx4Linear& d) { return bwd_layout(d).total; }
@@ -823,7 +825,7 @@ cudaError_t mx4_gemm_bwd(const void* dY, const Mx4View& x, const Mx4View& w, con
                          void* ws, int* status, cudaStream_t st) {
   const BwdWs l = bwd_layout(d);
   char* base = (char*)ws;
-  float* part = (float*)(base + l.part);
+  float *part_x = (float*)(base + l.part_x), *part_w = (float*)(base + l.part_w);
   const int64_t n_in = (int64_t)d.nb * d.in, n_out = (int64_t)d.nb * d.out;
   StageJob sj;
   const Operand a = staged(dY, d, d.out, base + l.dy, &sj);
@@ -837,27 +839,24 @@ cudaError_t mx4_gemm_bwd(const void* dY, const Mx4View& x, const Mx4View& w, con
   cudaError_t e = prepare(d, bj, dX != nullptr ? expand_job(w, base + l.w) : ExpandJob{}, dW != nullptr ? expand_job(x, base + l.x) : ExpandJob{},
                           sj, st);
   if (e != cudaSuccess) return e;
-  SumJob sums = {};
+  SumJob sum_x = {}, sum_w = {}, sum_b = {};
   if (dX != nullptr) {
     const Plan p = dx_plan(d);
-    e = product<false, true>(a, expanded(base + l.w, d.w()), Result{dX, d.rows, d.in, d.nb, n_in, d.in, 0}, nullptr, d, d.out, p, part,
-                             d.rows * n_in, status, st);
-    if (e == cudaSuccess && p.nsplit > 1) e = sum(d, SumJob{part, d.rows * n_in, p.nsplit, nullptr, 1, nullptr, 0, 0}, dX, nullptr, st);
+    e = product<false, true>(a, expanded(base + l.w, d.w()), Result{dX, d.rows, d.in, d.nb, n_in, d.in, 0}, nullptr, d, d.out, p, part_x,
+                             d.rows * n_in, false, status, st);
     if (e != cudaSuccess) return e;
+    if (p.nsplit > 1) sum_x = SumJob{part_x, dX, d.rows * n_in, p.nsplit, nullptr, 1};
   }
   if (dW != nullptr) {
     const Plan p = dw_plan(d);
+    // beside dX's product, if that went before: its operands were ready when that began
     e = product<true, true>(rows_as_k(a, d, d.out), expanded(base + l.x, d.x()), Result{dW, d.out, d.in, d.nb, d.in, (int64_t)d.out * d.in, 0},
-                            nullptr, d, d.rows, p, part, n_out * d.in, status, st);
+                            nullptr, d, d.rows, p, part_w, n_out * d.in, dX != nullptr, status, st);
     if (e != cudaSuccess) return e;
-    if (p.nsplit > 1) sums = SumJob{part, n_out * d.in, p.nsplit, nullptr, 1, nullptr, 0, 0};
+    if (p.nsplit > 1) sum_w = SumJob{part_w, dW, n_out * d.in, p.nsplit, nullptr, 1};
   }
-  if (dbias != nullptr && bj.nparts > 1) {
-    sums.bpart = bj.part;
-    sums.cols = n_out;
-    sums.nparts = bj.nparts;
-  }
-  return sum(d, sums, dW, dbias, st);
+  if (dbias != nullptr && bj.nparts > 1) sum_b = SumJob{bj.part, dbias, n_out, bj.nparts, nullptr, 1};
+  return sum(d.dtype, sum_x, sum_w, sum_b, st);
 }
 
 }  // namespace monarch
