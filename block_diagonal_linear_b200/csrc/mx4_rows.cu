@@ -163,7 +163,7 @@ __device__ __forceinline__ void product(float (&acc)[4], const uint32_t (&a0)[16
 constexpr int kAhead = 4;  // scale tiles of codes in flight
 
 template <typename TY, bool VEC>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, 2)
     mx4_token_kernel(const __nv_bfloat16* X, Mx4View w, int64_t rows, Mx4Out o, const TY* bias, TY* Y, int wk, bool w_early) {
   __shared__ float part[kWarps][16][9];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
