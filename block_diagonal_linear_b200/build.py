@@ -1,4 +1,5 @@
-"""Build libmonarch.so in-tree with nvcc for sm_100a.
+"""Build libmonarch.so in-tree with nvcc for sm_100a, and _mx4_native.so, the native half of the MX4
+binding, with g++ against the installed torch.
 
 Usage: python -m block_diagonal_linear_b200.build  (or call build()).
 """
@@ -15,6 +16,8 @@ LIB = os.path.join(PKG, "libmonarch.so")
 SOURCES = ["api.cu", "generic.cu", "tc_fwd.cu", "tc_rows.cu", "tc_wide.cu", "tc_split.cu", "tc_stage.cu", "tc_gemm.cu", "tc_pair.cu",
            "bwd_fast.cu", "bwd_gemm.cu", "linear.cu", "project.cu", "dyad.cu", "lattice.cu", "noalloc.cu",
            "mx4.cu", "mx4_quant.cu", "mx4_gemm.cu", "mx4_tc.cu", "mx4_rows.cu"]
+NATIVE_LIB = os.path.join(PKG, "_mx4_native.so")
+NATIVE_SOURCE = os.path.join(CSRC, "mx4_native.cpp")
 HEADERS = ["common.cuh", "ptx.cuh", "tc_common.cuh", "tc_gemm.cuh", "mx4.cuh"]
 
 NVCC_FLAGS = [
@@ -33,18 +36,35 @@ def _nvcc() -> str:
     return cand if os.path.exists(cand) else "nvcc"
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB):
+def _stale(target: str, sources) -> bool:
+    if not os.path.exists(target):
         return True
-    t = os.path.getmtime(LIB)
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
-    deps.append(os.path.join(ROOT, "include", "monarch.h"))
-    deps.append(os.path.abspath(__file__))
+    t = os.path.getmtime(target)
+    deps = [*sources, os.path.join(ROOT, "include", "monarch.h"), os.path.abspath(__file__)]
     return any(os.path.getmtime(p) > t for p in deps)
 
 
+def _build_native(verbose: bool):
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc())) or "/usr/local/cuda"
+    include = [os.path.join(base, "include"), os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    tmp = NATIVE_LIB + ".tmp%d" % os.getpid()
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch.compiled_with_cxx11_abi(), *(a for p in include for a in ("-isystem", p)),
+           NATIVE_SOURCE, "-o", tmp, "-L" + os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.check_call(cmd)
+    os.replace(tmp, NATIVE_LIB)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not _stale():
+    if force or _stale(NATIVE_LIB, [NATIVE_SOURCE]):
+        _build_native(verbose)
+    if not force and not _stale(LIB, [os.path.join(CSRC, f) for f in SOURCES + HEADERS]):
         return LIB
     objs = []
     bdir = os.path.join(PKG, "_build")

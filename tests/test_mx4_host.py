@@ -235,3 +235,45 @@ def test_binding_refuses_wrong_tensors():
     for bad in (dict(R=Lf), dict(L=R), dict(X=X[:, 1:]), dict(R=X), dict(Y=torch.zeros(5, 64))):
         with pytest.raises(ValueError):
             bdl.mx4_fwd(**{"X": X, "R": R, "L": Lf, "shape": shape, **bad})
+
+
+def test_binding_refuses_streams_and_memory_of_other_devices():
+    """Host checks ahead of any allocation: stand-ins for a stream and for another device's tensors."""
+    class Stream:
+        device = torch.device("cuda", 3)
+    W, X = fake(96, 2, 64, True), torch.zeros(5, 128, dtype=torch.bfloat16)
+    Xq = fake(5, 2, 64, False)
+    shape = dict(nb1=2, in1=64, out1=96, nb2=2, in2=96, out2=32, out_transpose=0)
+    for call in (lambda: bdl.mx4_quantise(X, nblocks=2, stream=Stream()), lambda: bdl.mx4_dequantise(Xq, stream=Stream()),
+                 lambda: bdl.mx4_linear_fwd(X, W, stream=Stream()), lambda: bdl.mx4_linear_fwd(Xq, W, stream=Stream()),
+                 lambda: bdl.mx4_linear_bwd(X, Xq, W, stream=Stream()),
+                 lambda: bdl.mx4_fwd(X, W, fake(32, 2, 96, True), shape, stream=Stream())):
+        with pytest.raises(ValueError, match="the stream is on cuda:3"):
+            call()
+    for call in (lambda: bdl.mx4_dequantise(Xq), lambda: bdl.mx4_linear_fwd(Xq, W)):  # memory of the host
+        with pytest.raises(ValueError, match="not on a CUDA device"):
+            call()
+    n = W.codes.numel()
+    with pytest.raises(ValueError, match="contiguous"):
+        bdl.Mx4(torch.zeros(2 * n, dtype=torch.uint8)[::2], W.scales, 96, 2, 64, True, "bf16")
+    with pytest.raises(ValueError, match="one device"):
+        bdl.Mx4(torch.zeros(n, dtype=torch.uint8, device="meta"), W.scales, 96, 2, 64, True, "bf16")
+    for bad in (0, -1, 3):
+        with pytest.raises(ValueError, match="do not divide"):
+            bdl.mx4_quantise(X, nblocks=bad)
+    for bad in (torch.float16, "fp8", 7):
+        with pytest.raises(ValueError, match="bf16 and f32"):
+            bdl.mx4_dequantise(Xq, bad)
+        with pytest.raises(ValueError, match="bf16 and f32"):
+            bdl.mx4_linear_fwd(Xq, W, dtype=bad)
+    with pytest.raises(ValueError, match="neither bfloat16 nor float32"):
+        bdl.mx4_quantise(X.half(), nblocks=2)
+    for bad in (None, 3.0, [1]):
+        with pytest.raises(ValueError):
+            bdl.mx4_quantise(bad)
+        with pytest.raises(ValueError):
+            bdl.mx4_linear_fwd(bad, W)
+        with pytest.raises(ValueError):
+            bdl.mx4_linear_bwd(bad, Xq, W)
+        with pytest.raises(ValueError):
+            bdl.mx4_dequantise(bad)
