@@ -8,7 +8,9 @@
 //
 // Tiles are 256 x 256 on CTA pairs (cta_group::2: each CTA loads 128 rows of X and 128 of W, 35 KB a stage
 // for its 128 x 256 share; alone it would load 51 KB, and what bounds a long product is the way from L2
-// to shared memory) or 128 x 64..256 on single CTAs where there are too few large ones.  A stage of the
+// to shared memory), or 128 x 64..256 on single CTAs where there are too few large ones or K is short; a CTA
+// may then keep the one tile of W it works on.  Short products are bound by Y's writes (10000 rows of four
+// 256 -> 1024 blocks: 17.0 us, a fill of Y alone 22).  A stage of the
 // ring holds 256 values of K as 128-byte swizzled rows, with the scale tiles (512 bytes for 128 rows x 128
 // values; a quantised tensor keeps them in the order that tcgen05.cp wants).  The MMA warp copies a
 // stage's scale tiles to TMEM and issues four MMAs of K = 64.  K beyond the tensor is filled with zero
@@ -23,7 +25,7 @@
 // epilogue: two warps a TMEM lane quadrant, one row a thread, alternate 128-byte chunks of columns.  Each
 // warp stages and stores its own 32 rows, so that no warp waits for another (with four warps that met at
 // barriers around a common staging buffer the epilogue bounded short K: 10000 rows of four 256 -> 1024
-// blocks took 28.4 us, now 20.4).
+// blocks took 28.4 us, so 20.4).
 #include "mx4.cuh"
 #include "tc_common.cuh"
 
@@ -45,29 +47,36 @@ struct Job {
   int64_t x_ratoms, w_ratoms;
 };
 
-template <int BN_, bool PAIR_>
+// KEEP: a CTA has one tile of W, whose up to four stages stay in shared memory, and every so many row tiles of
+// X; only X's stages come with every tile.
+template <int BN_, bool PAIR_, bool KEEP_ = false>
 struct Cfg {
-  static constexpr bool PAIR = PAIR_;
+  static constexpr bool PAIR = PAIR_, KEEP = KEEP_;
+  static_assert(!(PAIR && KEEP), "pairs share W's tiles already");
   static constexpr int BN = BN_, BM = PAIR ? 256 : 128;  // of a unit; a CTA holds 128 rows
   static constexpr int BROWS = PAIR ? BN / 2 : BN;       // rows of W that a CTA loads
   static constexpr int NT = BN >= 128 ? BN / 128 : 1;    // scale tiles of W per 128 values of K
   static constexpr int A_BYTES = 128 * 128, B_BYTES = BROWS * 128;
   static constexpr int SFA_BYTES = 1024, SFB_BYTES = 1024 * NT;
-  static constexpr int STAGE = A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES;
+  // X's part of a stage, and W's: behind it, or (KEEP) in a ring of its own behind X's
+  static constexpr int XSTAGE = A_BYTES + SFA_BYTES, WSTAGE = B_BYTES + SFB_BYTES;
+  static constexpr int STAGE = KEEP ? XSTAGE : XSTAGE + WSTAGE;
+  static constexpr int WPITCH = KEEP ? WSTAGE : STAGE, WKEPT = KEEP ? 4 : 0;
   static constexpr int SLOT1 = BN == 256 ? 216 : BN;     // first column of the second accumulator
-  // output slabs of a warp; a pair's long products want a fifth stage more than a second slab (8192 x 4096 -> 4096:
-  // 63.6 us with two, 60.6 with one), short ones the slab
-  static constexpr int SLABS = PAIR ? 1 : 2;
+  // output slabs of a warp; long products want a further stage more than a second slab (pairs, 8192 x 2048 -> 4096:
+  // 40.8 us with two, 38.1 with one), short ones the slab (singles, 128 inputs: 17.2 and 18.0)
+  static constexpr int SLABS = PAIR || KEEP ? 1 : 2;
   static constexpr int STG_BYTES = SLABS * kEpiWarps * kSlab;
   static constexpr int TAIL = 5120;
-  static constexpr int NSTAGE_RAW = (kSmemBudget - STG_BYTES - TAIL) / STAGE;
+  static constexpr int NSTAGE_RAW = (kSmemBudget - STG_BYTES - TAIL - WKEPT * WSTAGE) / STAGE;
   static constexpr int NSTAGE = NSTAGE_RAW > 8 ? 8 : NSTAGE_RAW;
-  static constexpr int SMEM_BYTES = STG_BYTES + NSTAGE * STAGE + TAIL + 1024;
+  static constexpr int SMEM_BYTES = STG_BYTES + NSTAGE * STAGE + WKEPT * WSTAGE + TAIL + 1024;
   static_assert(STAGE % 1024 == 0 && NSTAGE >= 2 && SLOT1 + BN <= (int)kSfCol && SMEM_BYTES <= 227 * 1024, "layout");
 };
 
 struct Bars {
   uint64_t full[8], empty[8];
+  uint64_t wfull[4];  // KEEP: of W's stages
   uint64_t acc_full[2];
   uint64_t acc_next;  // the next tile's accumulator may be written
   uint64_t mma_done;
@@ -90,8 +99,16 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
 struct Unit {
   int b, mt, nt;
 };
+template <bool KEEP>
 __device__ __forceinline__ Unit unit_at(const Job& j, int64_t unit) {
   Unit c;
+  if (KEEP) {  // a row tile of this CTA's tile of W
+    const uint32_t w = blockIdx.x % (uint32_t)(j.nb * j.ntiles);
+    c.nt = (int)(w % (uint32_t)j.ntiles);
+    c.b = (int)(w / (uint32_t)j.ntiles);
+    c.mt = (int)unit;
+    return c;
+  }
   uint32_t u = (uint32_t)unit;  // Y would be larger than any memory before this overflows; checked on the host
   c.nt = (int)(u % (uint32_t)j.ntiles);
   u /= (uint32_t)j.ntiles;
@@ -119,19 +136,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* stg = smem;
   uint8_t* ring = smem + C::STG_BYTES;
-  Bars* bars = (Bars*)(ring + C::NSTAGE * C::STAGE);
+  uint8_t* wring = ring + (C::KEEP ? C::NSTAGE * C::STAGE : C::XSTAGE);
+  Bars* bars = (Bars*)(ring + C::NSTAGE * C::STAGE + C::WKEPT * C::WSTAGE);
   int* abort_flag = &bars->abort_flag;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t rank = PAIR ? ptx::cluster_ctarank() : 0u;
   const bool first = rank == 0;
   const int64_t cl = PAIR ? blockIdx.x / 2 : blockIdx.x, ncl = PAIR ? gridDim.x / 2 : gridDim.x;
   const int nkb = (job.ksteps + 3) / 4;  // stages of a unit
+  // this CTA's units: every ncl-th; KEEP: row tiles, shared out among the CTAs with the same tile of W
+  const int64_t nw = C::KEEP ? (int64_t)job.nb * job.ntiles : 1;
+  const int64_t u0 = cl / nw, u1 = C::KEEP ? job.mtiles : job.units, ustep = C::KEEP ? (ncl - 1 - cl % nw) / nw + 1 : ncl;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NSTAGE; ++i) {
       ptx::mbar_init(&bars->full[i], 1);
       ptx::mbar_init(&bars->empty[i], 1);
     }
+    for (int i = 0; i < C::WKEPT; ++i) ptx::mbar_init(&bars->wfull[i], 1);
     for (int i = 0; i < 2; ++i) ptx::mbar_init(&bars->acc_full[i], 1);
     ptx::mbar_init(&bars->acc_next, (PAIR ? 2 : 1) * kEpiWarps);
     ptx::mbar_init(&bars->mma_done, 1);
@@ -167,42 +189,51 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t full0 = PAIR ? ptx::mapa_shared(ptx::smem_u32(&bars->full[0]), 0) : 0u;
       uint32_t it = 0;
       bool ok = true;
-      for (int64_t u = cl; u < job.units && ok; u += ncl) {
-        const Unit c = unit_at(job, u);
+      for (int64_t u = u0; u < u1 && ok; u += ustep) {
+        const Unit c = unit_at<C::KEEP>(job, u);
         const int xt = c.mt * (C::BM / 128) + (int)rank;  // this CTA's scale tile of X rows
         for (int kb = 0; kb < nkb; ++kb, ++it) {
           const int st = it % C::NSTAGE;
-          if (!wait_or_abort(&bars->empty[st], ((it / C::NSTAGE) & 1) ^ 1, abort_flag, status)) { ok = false; break; }
           uint8_t* sa = ring + st * C::STAGE;
-          uint8_t* sb = sa + C::A_BYTES;
-          uint8_t* sfa = sb + C::B_BYTES;
+          uint8_t* sb = wring + st * C::WPITCH;
           uint64_t* fl = &bars->full[st];
           const uint32_t fb = full0 + (uint32_t)(st * sizeof(uint64_t));
-          if (first) ptx::mbar_arrive_expect_tx(fl, (PAIR ? 2 : 1) * C::STAGE);
-          load3<PAIR>(sa, &tmX, fl, fb, kb * 128, xt * 128, c.b, pol);
-          load3<PAIR>(sb, &tmW, fl, fb, kb * 128, c.nt * C::BN + (int)rank * C::BROWS, c.b, pol);
           // two scale tiles of 128 values each: 128 words a tile; all of W's rows in both CTAs.  Tiles behind
           // the tensor are zeros, those behind a block belong to columns that are not stored.
-          load3<PAIR>(sfa, &tmSX, fl, fb, 0, 2 * kb, (int)(c.b * job.x_ratoms) + xt, pol);
-          load3<PAIR>(sfa + C::SFA_BYTES, &tmSW, fl, fb, 0, 2 * kb, (int)(c.b * job.w_ratoms) + c.nt * C::BN / 128, pol);
+          if (C::KEEP && u == u0) {
+            uint8_t* sw = wring + kb * C::WPITCH;
+            ptx::mbar_arrive_expect_tx(&bars->wfull[kb], C::WSTAGE);
+            load3<PAIR>(sw, &tmW, &bars->wfull[kb], 0, kb * 128, c.nt * C::BN, c.b, pol);
+            load3<PAIR>(sw + C::B_BYTES, &tmSW, &bars->wfull[kb], 0, 0, 2 * kb, (int)(c.b * job.w_ratoms) + c.nt * C::BN / 128, pol);
+          }
+          if (!wait_or_abort(&bars->empty[st], ((it / C::NSTAGE) & 1) ^ 1, abort_flag, status)) { ok = false; break; }
+          if (first) ptx::mbar_arrive_expect_tx(fl, (PAIR ? 2 : 1) * C::STAGE);
+          load3<PAIR>(sa, &tmX, fl, fb, kb * 128, xt * 128, c.b, pol);
+          if (!C::KEEP) load3<PAIR>(sb, &tmW, fl, fb, kb * 128, c.nt * C::BN + (int)rank * C::BROWS, c.b, pol);
+          load3<PAIR>(sa + C::A_BYTES, &tmSX, fl, fb, 0, 2 * kb, (int)(c.b * job.x_ratoms) + xt, pol);
+          if (!C::KEEP)
+            load3<PAIR>(sb + C::B_BYTES, &tmSW, fl, fb, 0, 2 * kb, (int)(c.b * job.w_ratoms) + c.nt * C::BN / 128, pol);
         }
       }
       if (!PAIR) {  // no copy may still be in flight when the CTA leaves (a pair's MMAs wait for theirs)
         const uint32_t issued = it;
         for (uint32_t k = (issued > (uint32_t)C::NSTAGE ? issued - C::NSTAGE : 0); k < issued; ++k)
           ptx::mbar_wait_bounded(&bars->full[k % C::NSTAGE], (k / C::NSTAGE) & 1, kWaitLimitNs);
+        if (C::KEEP)  // as many of W's as of X's first tile, at least
+          for (uint32_t k = 0; k < (uint32_t)nkb && k < issued + (ok ? 0 : 1); ++k)
+            ptx::mbar_wait_bounded(&bars->wfull[k], 0, kWaitLimitNs);
       }
     }
   } else if (warp == 1) {
     // ================================================================ MMA issuer (the pair's first CTA)
     if (first) {
       const uint32_t ring_s = ptx::smem_u32(ring);
-      const uint64_t dA = make_sdesc(ring_s, 1024, 2), dB = make_sdesc(ring_s + C::A_BYTES, 1024, 2);
-      const uint64_t dSA = scale_desc(ring_s + C::A_BYTES + C::B_BYTES);
-      const uint64_t dSB = scale_desc(ring_s + C::A_BYTES + C::B_BYTES + C::SFA_BYTES);
+      const uint32_t wring_s = ptx::smem_u32(wring);
+      const uint64_t dA = make_sdesc(ring_s, 1024, 2), dB = make_sdesc(wring_s, 1024, 2);
+      const uint64_t dSA = scale_desc(ring_s + C::A_BYTES), dSB = scale_desc(wring_s + C::B_BYTES);
       uint32_t it = 0, n = 0, sf = 0;
       bool ok = true;
-      for (int64_t u = cl; u < job.units && ok; u += ncl, ++n) {
+      for (int64_t u = u0; u < u1 && ok; u += ustep, ++n) {
         const int slot = n & 1;
         // the epilogue has begun the tile before this one (and so finished the one before that, whose
         // columns this tile takes) and has read the columns that the two share
@@ -210,12 +241,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tc_fence_after();
         const uint32_t d = tmem + slot * C::SLOT1;
         // BN = 64: every second tile takes the upper half of its scale tile's four columns
-        const uint32_t sfb_off = C::BN == 64 ? 2 * (uint32_t)(unit_at(job, u).nt & 1) : 0u;
+        const uint32_t sfb_off = C::BN == 64 ? 2 * (uint32_t)(unit_at<C::KEEP>(job, u).nt & 1) : 0u;
         for (int kb = 0; kb < nkb; ++kb, ++it) {
           const int st = it % C::NSTAGE;
           if (!all_wait_or_abort(&bars->full[st], (it / C::NSTAGE) & 1, abort_flag, status)) { ok = false; break; }
+          const int ws = C::KEEP ? kb : st;
+          if (C::KEEP && n == 0 && !all_wait_or_abort(&bars->wfull[ws], 0, abort_flag, status)) { ok = false; break; }
           ptx::tc_fence_after();
-          const uint64_t soff = (uint64_t)((st * C::STAGE) >> 4);
+          const uint64_t soff = (uint64_t)((st * C::STAGE) >> 4), woff = (uint64_t)((ws * C::WPITCH) >> 4);
           const int steps = job.ksteps - 4 * kb < 4 ? job.ksteps - 4 * kb : 4;
 #pragma unroll
           for (int a = 0; a < 2; ++a) {  // 128 values of K: scale tiles, then two MMAs
@@ -228,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               ptx::tmem_cp_32x128b_elect(sfa, dSA + soff + a * (512 >> 4));
 #pragma unroll
             for (int j = 0; j < C::NT; ++j) {
-              const uint64_t from = dSB + soff + ((j * 1024 + a * 512) >> 4);
+              const uint64_t from = dSB + woff + ((j * 1024 + a * 512) >> 4);
               if (PAIR)
                 ptx::tmem_cp_32x128b_pair_elect(sfb + j * 4, from);
               else
@@ -240,9 +273,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (kk >= steps) break;
               const uint32_t acc = (kb > 0 || kk > 0) ? 1u : 0u;
               if (PAIR)
-                ptx::mma_mxf4_ss_pair_elect(d, dA + soff + kk * 2, dB + soff + kk * 2, idesc_mxf4(C::BM, C::BN, k), sfa, sfb, acc);
+                ptx::mma_mxf4_ss_pair_elect(d, dA + soff + kk * 2, dB + woff + kk * 2, idesc_mxf4(C::BM, C::BN, k), sfa, sfb, acc);
               else
-                ptx::mma_mxf4_ss_elect(d, dA + soff + kk * 2, dB + soff + kk * 2, idesc_mxf4(C::BM, C::BN, k), sfa, sfb + sfb_off, acc);
+                ptx::mma_mxf4_ss_elect(d, dA + soff + kk * 2, dB + woff + kk * 2, idesc_mxf4(C::BM, C::BN, k), sfa, sfb + sfb_off, acc);
             }
           }
           if (PAIR)
@@ -278,17 +311,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int NB = MINE * CC / 32;
     float next_bias[NB];
     auto fetch_bias = [&](int64_t u) {
-      const Unit c = unit_at(job, u);
+      const Unit c = unit_at<C::KEEP>(job, u);
 #pragma unroll
       for (int i = 0; i < NB; ++i) {
         const int ch = (32 * i / CC) * 2 + half, col = c.nt * C::BN + ch * CC + (32 * i) % CC + lane;
-        next_bias[i] = u < job.units && ch < NCH && col < job.out ? mx4::load(bias + (int64_t)c.b * job.out + col) : 0.f;
+        next_bias[i] = u < u1 && ch < NCH && col < job.out ? mx4::load(bias + (int64_t)c.b * job.out + col) : 0.f;
       }
     };
-    if (bias != nullptr) fetch_bias(cl);
+    if (bias != nullptr) fetch_bias(u0);
     uint32_t n = 0, stored = 0;
-    for (int64_t u = cl; u < job.units; u += ncl, ++n) {
-      const Unit c = unit_at(job, u);
+    for (int64_t u = u0; u < u1; u += ustep, ++n) {
+      const Unit c = unit_at<C::KEEP>(job, u);
       const int slot = n & 1;
       const int n0 = c.nt * C::BN;
       const int64_t m0 = (int64_t)c.mt * C::BM + (int64_t)rank * 128 + quad * 32;  // this warp's rows
@@ -297,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < NB; ++i) bias_s[32 * i + lane] = next_bias[i];
         __syncwarp();
-        fetch_bias(u + ncl);  // asked for a tile ahead: the epilogue has no time to wait for it
+        fetch_bias(u + ustep);  // asked for a tile ahead: the epilogue has no time to wait for it
       }
       if (!all_wait_or_abort(&bars->acc_full[slot], (n >> 1) & 1, abort_flag, status)) break;
       ptx::tc_fence_after();
@@ -390,7 +423,8 @@ bool encode(CUtensorMap* m, CUtensorMapDataType type, const void* base, const cu
 bool code_map(CUtensorMap* m, const Mx4View& q, int box_rows) {
   return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, q.codes, {(cuuint64_t)q.s.pitch(), (cuuint64_t)q.s.rows, (cuuint64_t)q.s.nblocks},
                 {(cuuint64_t)q.s.pitch(), (cuuint64_t)q.s.pitch() * (cuuint64_t)q.s.rows}, {128, (cuuint32_t)box_rows, 1},
-                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+                CU_TENSOR_MAP_SWIZZLE_128B,
+                q.s.pitch() % 128 == 0 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_NONE);
 }
 // (words of a scale tile, tiles along K, tiles along the rows of all blocks), boxes of 2 x n tiles.
 bool scale_map(CUtensorMap* m, const Mx4View& q, int n) {
@@ -459,25 +493,37 @@ template <typename T>
 cudaError_t launch_type(const Mx4View& x, const Mx4View& w, const void* bias, const Mx4Linear& d, void* Y, int* status,
                         cudaStream_t st) {
   // The tile whose rounds over the SMs take the least time: a tile costs a stage's share of the way from
-  // L2 for every 256 inputs, and its epilogue.  Microseconds from 8192 rows -> 4096 (256 x 256 pairs,
-  // 128 x 256 single): 19.7 and 14.1 with 256 inputs, 22.2 and 17.7 with 512, 27.1 and 26.6 with 1024, 60.6 and 75 with
-  // 4096; a pair's two CTAs wait for each other once a tile, which only a long K hides.
+  // L2 for every 256 inputs, and its epilogue.  Microseconds from 8192 rows -> 4096 (256 x 256 pairs, 128 x 256
+  // single, 128 x 256 with W kept): 19.8, 14.0 and 15.0 with 256 inputs, 22.5, 17.5 and 17.2 with 512, 26.9, 27.4 and
+  // 24.9 with 1024; 62.7 and 66.7 with 4096, where W does not fit.  A pair's two CTAs wait for each other once a
+  // tile, which only a long K hides; with W kept there is one tile of W a CTA, which costs rounds.  TMA takes rows
+  // of codes whose pitch is no multiple of 32 bytes in smaller pieces (single and kept with 96 inputs 22.0 and 16.6).
   struct Tile {
     int bm, bn;
     double stage, fixed;
   };
   const Tile tiles[4] = {{256, 256, 0.46, 2.3}, {128, 256, 0.62, 1.3}, {128, 128, 0.42, 1.0}, {128, 64, 0.30, 0.8}};
+  const double part = x.s.pitch() % 32 != 0 ? 1.2 : x.s.pitch() % 128 != 0 ? 0.33 : 0.0;  // for a short last stage
+  const int stages = (x.s.cols + 255) / 256;
   int best = 0;
   double least = 1e30;
   for (int i = 0; i < 4; ++i) {
     if (i < 3 && d.out <= tiles[i].bn / 2) continue;  // half of it or more would be empty
     const int64_t units = (d.rows + tiles[i].bm - 1) / tiles[i].bm * d.nb * ((d.out + tiles[i].bn - 1) / tiles[i].bn);
     const int64_t slots = i == 0 ? num_sms() / 2 : num_sms();
-    const double t = (double)((units + slots - 1) / slots) * ((x.s.cols + 255) / 256 * tiles[i].stage + tiles[i].fixed);
+    const double t = (double)((units + slots - 1) / slots) * (stages * tiles[i].stage + tiles[i].fixed + part * tiles[i].bn / 256);
     if (t < least) {
       least = t;
       best = i;
     }
+  }
+  // W kept: where its tiles are full ones, so that no CTA has a lighter one than the others, and every 32-byte
+  // sector of Y has one writer (the CTAs of a row are at different rows: sixteen 90 -> 250 blocks 82 us, 64 without)
+  const int64_t wtiles = (int64_t)d.nb * ((d.out + 255) / 256), share = num_sms() / wtiles;
+  if (stages <= 4 && share > 0 && d.out >= (d.out + 255) / 256 * 230 && (int64_t)d.out * sizeof(T) % 32 == 0) {
+    const int64_t mtiles = (d.rows + 127) / 128, rounds = (mtiles + share - 1) / share;
+    if ((double)rounds * (stages * 0.33 + 1.6) + stages * 0.35 < least)
+      return launch<Cfg<256, false, true>, T, true>(x, w, bias, d, Y, status, st);
   }
   switch (best) {
     case 0: return launch_out<256, true, T>(x, w, bias, d, Y, status, st);

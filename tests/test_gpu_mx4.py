@@ -146,6 +146,14 @@ def test_linear_forward_both_quantised(rows, nb, inn, out, bias, dtype):
     assert torch.equal(Y, bdl.mx4_linear_fwd(Xq, Wq, bias=t["b"]))
 
 
+# one to four stages of K over many row tiles (a tile of W is kept), last tiles of rows and columns not full
+@pytest.mark.parametrize("rows,nb,inn,out,bias,dtype", [
+    (19001, 1, 90, 256, True, "bf16"), (19001, 1, 90, 256, True, "f32"), (6000, 2, 288, 1000, False, "f32"),
+    (1300, 1, 700, 3840, True, "bf16"), (2333, 1, 1000, 2000, True, "bf16"), (19011, 1, 1024, 240, False, "bf16")])
+def test_linear_forward_of_many_rows(rows, nb, inn, out, bias, dtype):
+    test_linear_forward_both_quantised(rows, nb, inn, out, bias, dtype)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("rows,nb,inn,out,bias", LAYERS)
 def test_linear_forward_weights_only(rows, nb, inn, out, bias, dtype):
