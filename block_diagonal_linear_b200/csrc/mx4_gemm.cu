@@ -440,20 +440,21 @@ __device__ __forceinline__ void stage_rows(const StageJob& j, int64_t blk) {
 }
 
 // part[k][c] = sum of rows [k * kBiasRows, + kBiasRows) of dY's column c, in a fixed order: a warp takes
-// every eighth row, a lane 16 bytes of it (or one element where rows are no multiple of 16 bytes).  With one
-// part the sums are dbias.
+// every eighth row, a lane 16 bytes of it, or, where rows are no multiple of 16 bytes, 8 columns out of the
+// aligned words that cover them (2683 rows of 20646 in bf16: 18 us beside their staging, 48 element by element), or
+// one column where that would leave most SMs without work (301 rows of 1665 in fp32: 14 us for the whole backward
+// pass, 24 with 8 columns).  With one part the sums are dbias.
 constexpr int kBiasRows = 256;
 struct BiasJob {
   const void* dY;
   float* part;
   void* dbias;
   int64_t rows, cols;
-  int cgroups;
+  int lane, cgroups;  // columns of a lane; groups of 32 lanes
   int64_t nparts, blocks;
 };
-template <typename T, bool VEC>
+template <typename T, int W, bool VEC>
 __device__ __forceinline__ void bias_part(const BiasJob& j, int64_t blk, float (*sums)[32 * 8]) {
-  constexpr int W = VEC ? 16 / sizeof(T) : 1;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int64_t k = blk / j.cgroups;
   const int64_t c0 = (blk - k * j.cgroups) * (32 * W), c = c0 + lane * W;
@@ -461,31 +462,33 @@ __device__ __forceinline__ void bias_part(const BiasJob& j, int64_t blk, float (
   const T* p = (const T*)j.dY + c;
   float acc[W] = {};
   if (c < j.cols) {
-    constexpr int U = 8;  // rows in flight
+    constexpr int U = VEC || W == 1 ? 8 : sizeof(T) == 2 ? 4 : 2, N = (W * sizeof(T) + 3) / 4;  // rows in flight, words of a lane's columns
+    const T* end = (const T*)j.dY + j.rows * j.cols;
     for (int64_t r = r0 + warp; r < r1; r += 8 * U) {
-      if (VEC) {
-        uint4 v[U];
+      uint32_t v[U][8];
 #pragma unroll
-        for (int u = 0; u < U; ++u) v[u] = r + 8 * u < r1 ? *(const uint4*)(p + (r + 8 * u) * j.cols) : make_uint4(0, 0, 0, 0);
+      for (int u = 0; u < U; ++u) {
+        const bool live = r + 8 * u < r1;
+        if (VEC) {
+          const uint4 q = live ? *(const uint4*)(p + (r + 8 * u) * j.cols) : make_uint4(0, 0, 0, 0);
+          v[u][0] = q.x, v[u][1] = q.y, v[u][2] = q.z, v[u][3] = q.w;
+        } else if (W == 1) {
+          v[u][0] = live ? __float_as_uint(mx4::load(p + (r + 8 * u) * j.cols)) : 0u;
+        } else {
+          mx4::load8_any(p + (r + 8 * u) * j.cols, live ? (int)min((int64_t)8, j.cols - c) : 0, end, v[u]);
+        }
+      }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+      for (int u = 0; u < U; ++u) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (sizeof(T) == 2) {
-              acc[(2 * i) % W] += __uint_as_float(w[i] << 16);
-              acc[(2 * i + 1) % W] += __uint_as_float(w[i] & 0xffff0000u);
-            } else {
-              acc[i % W] += __uint_as_float(w[i]);
-            }
+        for (int i = 0; i < N; ++i) {
+          if (sizeof(T) == 2 && W > 1) {
+            acc[(2 * i) % W] += __uint_as_float(v[u][i] << 16);
+            acc[(2 * i + 1) % W] += __uint_as_float(v[u][i] & 0xffff0000u);
+          } else {
+            acc[i % W] += __uint_as_float(v[u][i]);
           }
         }
-      } else {
-        float v[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) v[u] = r + 8 * u < r1 ? mx4::load(p + (r + 8 * u) * j.cols) : 0.f;
-#pragma unroll
-        for (int u = 0; u < U; ++u) acc[0] += v[u];
       }
     }
   }
@@ -514,9 +517,11 @@ __global__ void __launch_bounds__(256, 4)  // the most demanding job must not co
   int64_t blk = blockIdx.x;
   if (blk < bias.blocks) {
     if (bias.cols * sizeof(T) % 16 == 0)
-      bias_part<T, true>(bias, blk, sums);
+      bias_part<T, 16 / sizeof(T), true>(bias, blk, sums);
+    else if (bias.lane == 8)
+      bias_part<T, 8, false>(bias, blk, sums);
     else
-      bias_part<T, false>(bias, blk, sums);
+      bias_part<T, 1, false>(bias, blk, sums);
     return;
   }
   blk -= bias.blocks;
@@ -832,8 +837,9 @@ cudaError_t mx4_gemm_bwd(const void* dY, const Mx4View& x, const Mx4View& w, con
   if (dX == nullptr && dW == nullptr) sj.blocks = 0;
   BiasJob bj = {};
   if (dbias != nullptr) {
-    const int es = d.dtype == MONARCH_BF16 ? 2 : 4, lane = n_out * es % 16 == 0 ? 16 / es : 1;  // columns a lane
-    bj = BiasJob{dY, (float*)(base + l.bias), dbias, d.rows, n_out, (int)((n_out + 32 * lane - 1) / (32 * lane)), bias_parts(d), 0};
+    const int es = d.dtype == MONARCH_BF16 ? 2 : 4;
+    const int lane = n_out * es % 16 == 0 ? 16 / es : bias_parts(d) * ((n_out + 255) / 256) >= 2 * num_sms() ? 8 : 1;
+    bj = BiasJob{dY, (float*)(base + l.bias), dbias, d.rows, n_out, lane, (int)((n_out + 32 * lane - 1) / (32 * lane)), bias_parts(d), 0};
     bj.blocks = bj.nparts * bj.cgroups;
   }
   cudaError_t e = prepare(d, bj, dX != nullptr ? expand_job(w, base + l.w) : ExpandJob{}, dW != nullptr ? expand_job(x, base + l.x) : ExpandJob{},

@@ -12,12 +12,13 @@
 // up to four scale tiles of codes before it uses the first.  The inputs are split up to 8 ways, and the
 // shares' sums join in a fixed order.
 //
-// Up to 8 bf16 tokens (mx4_token_kernel) the shares are warps of a CTA and a lane reads its inputs where
-// they are: the weight is all there is to read.  More tokens, or fp32 ones (mx4_batch_kernel, up to 64 a
-// pass), would have every warp gather and cut its own inputs again, 16 bytes from 16 lines a load (4096 ->
-// 4096: 18.5 us for 32 bf16 tokens against 12.0, 14.8 for one in fp32); there the shares are CTAs of a
-// cluster, and a CTA's 8 warps take 128 outputs and share one copy of the inputs in shared memory, already
-// cut into parts, in the order in which lanes read it.
+// Up to 8 bf16 tokens, and more where the weight is small (mx4_token_kernel), the shares are warps of a CTA
+// and a lane reads its inputs where they are.  Warps that are left take further tiles, or neighbouring blocks: of
+// a transposed result (a Monarch stage) these lie next to each other (32 tokens through sixty-four 64 x 64 blocks
+// twice: 5.1 us, 13.5 with a block a CTA).  With a large weight every warp would gather and cut its own inputs
+// too often (4096 -> 4096: 16.5 us for 32 bf16 tokens against 12.2, 12.2 for one in fp32 against 8.1); there
+// (mx4_batch_kernel, up to 64 tokens a pass) the shares are CTAs of a cluster, and a CTA's 8 warps take 128 outputs
+// and share one copy of the inputs in shared memory, already cut into parts, in the order in which lanes read it.
 #include "mx4.cuh"
 #include "tc_common.cuh"
 
@@ -162,62 +163,74 @@ __device__ __forceinline__ void product(float (&acc)[4], const uint32_t (&a0)[16
 
 constexpr int kAhead = 4;  // scale tiles of codes in flight
 
-template <typename TY, bool VEC>
-__global__ void __launch_bounds__(kWarps * 32, 2)
-    mx4_token_kernel(const __nv_bfloat16* X, Mx4View w, int64_t rows, Mx4Out o, const TY* bias, TY* Y, int wk, bool w_early) {
-  __shared__ float part[kWarps][16][9];
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-  const int kw = warp % wk, mw = warp / wk;  // this warp's share of the inputs, and its 16 outputs
-  const int per = blockDim.x / 32 / wk;      // output tiles of the CTA
-  const int64_t tile0 = (int64_t)blockIdx.x * per;
-  const int b = blockIdx.y;
-  const CodeRows cr(w, b, (tile0 + mw) * 16 + g, t);
-  const __nv_bfloat16* p = X + (int64_t)g * w.s.nblocks * w.s.cols + (int64_t)b * w.s.cols + t * 32;
+constexpr int kPlane = 16 * 9 + 4;  // a warp's sums, 16 outputs x 8 tokens: padded, 8 blocks x 4 outputs in 32 banks
 
-  const __nv_bfloat16* end = X + rows * w.s.nblocks * w.s.cols;
+// Warps of a CTA: 2^lk shares of the inputs, 2^lb neighbouring blocks, `per` tiles of 16 outputs; 8 tokens.
+template <typename TX, int PARTS, typename TY, bool VEC, int AHEAD>
+__global__ void __launch_bounds__(kWarps * 32, 2)
+    mx4_token_kernel(const TX* X, Mx4View w, int64_t rows, Mx4Out o, const TY* bias, TY* Y, int lk, int lb, int per, bool w_early) {
+  __shared__ float part[kWarps * kPlane];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+  const int wk = 1 << lk, nbw = 1 << lb;
+  const int kw = warp & (wk - 1), bw = (warp >> lk) & (nbw - 1), mw = warp >> (lk + lb);
+  const int64_t tile0 = (int64_t)blockIdx.x * per, r0 = (int64_t)blockIdx.z * 8, r = r0 + g;
+  const int b0 = blockIdx.y * nbw, b = min(b0 + bw, w.s.nblocks - 1);
+  CodeRows cr(w, b, (tile0 + mw) * 16 + g, t);
+  if (mw >= per) cr.katoms = 0;  // nothing to do but the join
+  const int64_t pitch = (int64_t)w.s.nblocks * w.s.cols;
+  const TX *p = X + r * pitch + (int64_t)b * w.s.cols + t * 32, *end = X + rows * pitch;
 
   float acc[4] = {};
-  Codes c[kAhead];
+  Codes c[AHEAD];
   // weights that no kernel of this stream is still writing may be asked for ahead of the wait
   if (!w_early) ptx::griddep_wait();
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i) c[i] = cr.at(kw + i * wk);
+  for (int i = 0; i < AHEAD; ++i) c[i] = cr.at(kw + i * wk);
   if (w_early) ptx::griddep_wait();
   ptx::griddep_launch_dependents();
 
-  for (int ka0 = kw; ka0 < cr.katoms; ka0 += kAhead * wk) {
-    if (ka0 != kw) {
+#pragma unroll 1
+  for (int ka0 = kw; ka0 < cr.katoms; ka0 += AHEAD * wk) {
+    if (AHEAD > 1 && ka0 != kw) {
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) c[i] = cr.at(ka0 + i * wk);
+      for (int i = 0; i < AHEAD; ++i) c[i] = cr.at(ka0 + i * wk);
     }
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
+    for (int i = 0; i < AHEAD; ++i) {
       const int ka = ka0 + i * wk;
       if (ka >= cr.katoms) break;
       uint32_t x[4][8], a0[16], a1[16];
 #pragma unroll
-      for (int v = 0; v < 4; ++v) load8<VEC>(p + ka * 128 + 8 * v, g < rows ? w.s.cols - ka * 128 - t * 32 - 8 * v : 0, end, x[v]);
+      for (int v = 0; v < 4; ++v) load8<VEC>(p + ka * 128 + 8 * v, r < rows ? w.s.cols - ka * 128 - t * 32 - 8 * v : 0, end, x[v]);
       values(c[i], t, a0, a1);
+      if (AHEAD == 1) c[0] = cr.at(ka + wk);
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
-        uint32_t bp[1][4];
-        split8<1>(x[v], bp, (const __nv_bfloat16*)nullptr);
-        product<1>(acc, a0, a1, v, bp);
+        uint32_t bp[PARTS][4];
+        split8<PARTS>(x[v], bp, (const TX*)nullptr);
+        product<PARTS>(acc, a0, a1, v, bp);
       }
     }
   }
 #pragma unroll
-  for (int e = 0; e < 4; ++e) part[warp][g + 8 * (e >> 1)][2 * t + (e & 1)] = acc[e];
+  for (int e = 0; e < 4; ++e) part[warp * kPlane + (g + 8 * (e >> 1)) * 9 + 2 * t + (e & 1)] = acc[e];
   __syncthreads();
-  // join the shares in order; consecutive threads take consecutive outputs of one token
-  for (int e = threadIdx.x; e < per * 128; e += blockDim.x) {
-    const int row = e % 16, tile = (e / 16) % per, n = e / (16 * per);
-    const int64_t out = (tile0 + tile) * 16 + row;
-    if (out >= w.s.rows || n >= rows) continue;
+  // join the shares in order; consecutive threads take neighbours in Y: outputs, or blocks where it is transposed.
+  // A thread has one output of every so many tokens.
+  const int m = threadIdx.x & ((128 >> lk) - 1);
+  const int row = o.n == 1 ? m & 15 : (m >> lb) & 15, q = o.n == 1 ? m >> (7 - lk - lb) : m & (nbw - 1);
+  const int tile = o.n == 1 ? (m >> 4) & ((kWarps >> (lk + lb)) - 1) : m >> (4 + lb);
+  const int64_t out = (tile0 + tile) * 16 + row;
+  if (tile >= per || out >= w.s.rows || b0 + q >= w.s.nblocks) return;
+  const float add = bias != nullptr ? mx4::load(bias + (int64_t)(b0 + q) * w.s.rows + out) : 0.f;
+  const float* sum = part + (((tile << lb) + q) << lk) * kPlane + row * 9;
+  TY* y = Y + o.at(b0 + q, r0, out);
+  const int tokens = (int)min((int64_t)8, rows - r0);
+#pragma unroll 4
+  for (int n = threadIdx.x >> (7 - lk); n < tokens; n += 2 << lk) {
     float v = 0.f;
-    for (int k = 0; k < wk; ++k) v += part[tile * wk + k][row][n];
-    if (bias != nullptr) v += mx4::load(bias + (int64_t)b * w.s.rows + out);
-    st_from_f32(Y + o.at(b, n, out), v);
+    for (int k = 0; k < wk; ++k) v += sum[k * kPlane + n];
+    st_from_f32(y + n * o.m, v + add);
   }
 }
 
@@ -353,20 +366,24 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   ptx::cluster_sync_all();  // the others may still read this CTA's sums
 }
 
-int shares_for(const Mx4View& w) {
-  int shares = 1;
-  while (shares < 8 && shares * 2 <= w.s.katoms()) shares *= 2;
-  return shares;
-}
-
-template <typename TY, bool VEC>
+template <typename TX, int PARTS, typename TY, bool VEC>
 cudaError_t launch_token(const void* X, const Mx4View& w, const void* bias, int64_t rows, const Mx4Out& o, void* Y, bool w_early,
                          cudaStream_t st) {
-  const int wk = shares_for(w);
   const int64_t mtiles = (w.s.rows + 15) / 16;
-  const int per = (int)(mtiles < kWarps / wk ? mtiles : kWarps / wk);
-  return launch_kernel(mx4_token_kernel<TY, VEC>, dim3((unsigned)((mtiles + per - 1) / per), (unsigned)w.s.nblocks),
-                       dim3(wk * per * 32), 0, st, true, (const __nv_bfloat16*)X, w, rows, o, (const TY*)bias, (TY*)Y, wk, w_early);
+  int lk = 0, lb = 0;
+  while (lk < 3 && 2 << lk <= w.s.katoms()) ++lk;
+  // neighbouring blocks: in place of tiles where these are fewer or where the result is transposed
+  while (lk + lb < 3 && 2 << lb <= w.s.nblocks && (o.n != 1 || mtiles << (lk + lb) < kWarps)) ++lb;
+  const int room = kWarps >> (lk + lb), per = (int)(mtiles < room ? mtiles : room);
+  const dim3 grid((unsigned)((mtiles + per - 1) / per), (unsigned)((w.s.nblocks + (1 << lb) - 1) >> lb), (unsigned)((rows + 7) / 8));
+  const dim3 block(kWarps * 32);
+  // shares of one or two scale tiles run quicker in less code (16 tokens of 1024 -> 1024: 2.1 us, 2.4 with four
+  // tiles ahead), the longest want the loads (8 of 4096 -> 4096 in fp32: 15.2 us and 18.1 without)
+  return w.s.katoms() <= 2 << lk
+             ? launch_kernel(mx4_token_kernel<TX, PARTS, TY, VEC, 1>, grid, block, 0, st, true, (const TX*)X, w, rows, o,
+                             (const TY*)bias, (TY*)Y, lk, lb, per, w_early)
+             : launch_kernel(mx4_token_kernel<TX, PARTS, TY, VEC, kAhead>, grid, block, 0, st, true, (const TX*)X, w, rows, o,
+                             (const TY*)bias, (TY*)Y, lk, lb, per, w_early);
 }
 
 template <typename TX, int PARTS, typename TY, bool VEC, int NT>
@@ -403,11 +420,15 @@ cudaError_t launch_batch(const void* X, const Mx4View& w, const void* bias, int6
 template <typename TX, int PARTS, typename TY, bool VEC>
 cudaError_t launch_vec(const void* X, const Mx4View& w, const void* bias, int64_t rows, const Mx4Out& o, void* Y, bool w_early,
                        cudaStream_t st) {
-  if (rows <= 8) {
-    if constexpr (PARTS == 1)
-      return launch_token<TY, VEC>(X, w, bias, rows, o, Y, w_early, st);
-    else
-      return launch_batch<TX, PARTS, TY, VEC, 1>(X, w, bias, rows, o, Y, w_early, st);
+  // The direct kernel, as long as cutting inputs and expanding codes again and again is little work: every 8 tokens
+  // do it for every 16 outputs.  us, direct and batch: 32 bf16 tokens of sixty-four 64 -> 64 blocks 2.2 and 4.1, of
+  // 1024 -> 1024 2.6 and 5.3, of 1024 -> 4096 7.9 and 7.2, of 4096 -> 4096 16.5 and 12.2; 33 of four 250 -> 1000 blocks
+  // 5.7 and 6.9; 16 fp32 tokens of 1024 -> 1024 3.8 and 5.2, of 1024 -> 4096 10.1 and 6.9
+  const int64_t work = (int64_t)w.s.nblocks * w.s.rows * w.s.cols * ((rows + 7) / 8) * PARTS;
+  if ((PARTS == 1 && rows <= 8) || work <= (VEC ? 10 << 20 : 6 << 20))
+    return launch_token<TX, PARTS, TY, VEC>(X, w, bias, rows, o, Y, w_early, st);
+  if constexpr (PARTS > 1) {
+    if (rows <= 8) return launch_batch<TX, PARTS, TY, VEC, 1>(X, w, bias, rows, o, Y, w_early, st);
   }
   if (rows <= 16) return launch_batch<TX, PARTS, TY, VEC, 2>(X, w, bias, rows, o, Y, w_early, st);
   if constexpr (PARTS == 1) {
