@@ -7,10 +7,11 @@
 // fp32 sum, so the result is rounded once, in the epilogue.
 //
 // Tiles are 256 x 256 on CTA pairs (cta_group::2: each CTA loads 128 rows of X and 128 of W, 35 KB a stage
-// for its 128 x 256 share; alone it would load 51 KB, and what bounds a long product is the way from L2
-// to shared memory), or 128 x 64..256 on single CTAs where there are too few large ones or K is short; a CTA
-// may then keep the one tile of W it works on.  Short products are bound by Y's writes (10000 rows of four
-// 256 -> 1024 blocks: 17.0 us, a fill of Y alone 22).  A stage of the
+// for its 128 x 256 share; alone it would load 51 KB), or 128 x 64..256 on single CTAs where there are too few
+// large ones or K is short; a CTA may then keep the one tile of W it works on.  A long product (8192 x 4096 ->
+// 4096: 62.9 us) is bound by the MMAs, 46 us with everything else left out; waiting for loads adds 7, the scale
+// copies, which take turns with the MMAs, 5, the epilogue 5.  Short ones are bound by Y's writes (10000 rows of
+// four 256 -> 1024 blocks: 17.0 us, a library's fill of Y alone 22).  A stage of the
 // ring holds 256 values of K as 128-byte swizzled rows, with the scale tiles (512 bytes for 128 rows x 128
 // values; a quantised tensor keeps them in the order that tcgen05.cp wants).  The MMA warp copies a
 // stage's scale tiles to TMEM and issues four MMAs of K = 64.  K beyond the tensor is filled with zero

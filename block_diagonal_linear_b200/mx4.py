@@ -31,7 +31,7 @@ def _load():
     try:
         from . import _mx4_native
     except ImportError as e:
-        raise RuntimeError("_mx4_native.so is not built for this torch; run `python -m block_diagonal_linear_b200.build`") from e
+        raise RuntimeError("_mx4_native.so is not built for this torch; run `python -m block_diagonal_linear_b200.build --force`") from e
     _mx4_native.init(tuple(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in _ENTRY_POINTS), _check)
     return _mx4_native
 
@@ -64,6 +64,9 @@ class Mx4:
         self._hold = (codes, scales)
         self._raw = _RAW.pack(codes.data_ptr(), scales.data_ptr(), self.rows, self.nblocks, self.cols, self.by_block, self.code,
                               codes.get_device() if codes.is_cuda else -1)
+
+    def __reduce__(self):  # copies and pickles: _raw belongs to this object's memory alone
+        return Mx4, (self.codes, self.scales, self.rows, self.nblocks, self.cols, self.by_block, self.code)
 
     @property
     def codes(self):

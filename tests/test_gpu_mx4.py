@@ -460,3 +460,14 @@ def test_large_offsets():
     close(Y[-3:], ref, mags, cols + 2, "bf16", "Y")
     back = bdl.mx4_dequantise(q)
     assert np.array_equal(f64(back[-3:]), oracle.mx4_round(v)) and not back[:16].any()
+
+
+def test_a_copied_weight_outlives_the_first():
+    import copy
+    t, v = layer(5, 2, 96, 64, False, "bf16")
+    Wq = bdl.mx4_quantise(t["W"])
+    want = bdl.mx4_linear_fwd(t["X"], Wq)
+    twin = copy.deepcopy(Wq)
+    Wq.codes.zero_()
+    assert torch.equal(bdl.mx4_linear_fwd(t["X"], twin), want)
+    check_forward(want, v["x"], v, 96, "bf16", "Y")

@@ -277,3 +277,17 @@ def test_binding_refuses_streams_and_memory_of_other_devices():
             bdl.mx4_linear_bwd(bad, Xq, W)
         with pytest.raises(ValueError):
             bdl.mx4_dequantise(bad)
+
+
+def test_copies_have_memory_of_their_own():
+    import copy
+    import pickle
+    q = fake(96, 2, 64, True)
+    q.codes[3] = 7
+    for c in (copy.deepcopy(q), pickle.loads(pickle.dumps(q))):
+        assert c.codes.data_ptr() != q.codes.data_ptr() and torch.equal(c.codes, q.codes) and torch.equal(c.scales, q.scales)
+        assert c._raw != q._raw and c._raw[16:] == q._raw[16:]
+        assert int.from_bytes(c._raw[:8], "little") == c.codes.data_ptr()
+        assert int.from_bytes(c._raw[8:16], "little") == c.scales.data_ptr()
+        assert (c.shape, c.dtype, c.nbytes) == (q.shape, q.dtype, q.nbytes)
+    assert copy.copy(q)._raw == q._raw
