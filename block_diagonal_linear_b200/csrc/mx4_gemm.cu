@@ -442,7 +442,7 @@ __device__ __forceinline__ void stage_rows(const StageJob& j, int64_t blk) {
 }
 
 // part[k][c] = sum of rows [k * kBiasRows, + kBiasRows) of dY's column c, in a fixed order: a warp takes
-// every eighth row, a lane 16 bytes of it, or, where rows are no multiple of 16 bytes, 8 columns out of the
+// every NW-th row, a lane 16 bytes of it, or, where rows are no multiple of 16 bytes, 8 columns out of the
 // aligned words that cover them (2683 rows of 20646 in bf16: 18 us beside their staging, 48 element by element), or
 // one column where that would leave most SMs without work (301 rows of 1665 in fp32: 14 us for the whole backward
 // pass, 24 with 8 columns).  With one part the sums are dbias.
@@ -455,7 +455,7 @@ struct BiasJob {
   int lane, cgroups;  // columns of a lane; groups of 32 lanes
   int64_t nparts, blocks;
 };
-template <typename T, int W, bool VEC>
+template <typename T, int W, bool VEC, int NW>
 __device__ __forceinline__ void bias_part(const BiasJob& j, int64_t blk, float (*sums)[32 * 8]) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int64_t k = blk / j.cgroups;
@@ -466,18 +466,18 @@ __device__ __forceinline__ void bias_part(const BiasJob& j, int64_t blk, float (
   if (c < j.cols) {
     constexpr int U = VEC || W == 1 ? 8 : sizeof(T) == 2 ? 4 : 2, N = (W * sizeof(T) + 3) / 4;  // rows in flight, words of a lane's columns
     const T* end = (const T*)j.dY + j.rows * j.cols;
-    for (int64_t r = r0 + warp; r < r1; r += 8 * U) {
+    for (int64_t r = r0 + warp; r < r1; r += NW * U) {
       uint32_t v[U][8];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const bool live = r + 8 * u < r1;
+        const bool live = r + NW * u < r1;
         if (VEC) {
-          const uint4 q = live ? *(const uint4*)(p + (r + 8 * u) * j.cols) : make_uint4(0, 0, 0, 0);
+          const uint4 q = live ? *(const uint4*)(p + (r + NW * u) * j.cols) : make_uint4(0, 0, 0, 0);
           v[u][0] = q.x, v[u][1] = q.y, v[u][2] = q.z, v[u][3] = q.w;
         } else if (W == 1) {
-          v[u][0] = live ? __float_as_uint(mx4::load(p + (r + 8 * u) * j.cols)) : 0u;
+          v[u][0] = live ? __float_as_uint(mx4::load(p + (r + NW * u) * j.cols)) : 0u;
         } else {
-          mx4::load8_any(p + (r + 8 * u) * j.cols, live ? (int)min((int64_t)8, j.cols - c) : 0, end, v[u]);
+          mx4::load8_any(p + (r + NW * u) * j.cols, live ? (int)min((int64_t)8, j.cols - c) : 0, end, v[u]);
         }
       }
 #pragma unroll
@@ -497,16 +497,37 @@ __device__ __forceinline__ void bias_part(const BiasJob& j, int64_t blk, float (
 #pragma unroll
   for (int i = 0; i < W; ++i) sums[warp][lane * W + i] = acc[i];
   __syncthreads();
-  for (int e = threadIdx.x; e < 32 * W; e += 256) {
+  for (int e = threadIdx.x; e < 32 * W; e += 32 * NW) {
     if (c0 + e >= j.cols) break;
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) v += sums[w][e];
+    for (int w = 0; w < NW; ++w) v += sums[w][e];
     if (j.nparts == 1)
       st_from_f32((T*)j.dbias + c0 + e, v);
     else
       j.part[k * j.cols + c0 + e] = v;
   }
+}
+
+template <typename T, int NW>
+__device__ __forceinline__ void bias_block(const BiasJob& j, int64_t blk, float (*sums)[32 * 8]) {
+  if (j.cols * sizeof(T) % 16 == 0)
+    bias_part<T, 16 / sizeof(T), true, NW>(j, blk, sums);
+  else if (j.lane == 8)
+    bias_part<T, 8, false, NW>(j, blk, sums);
+  else
+    bias_part<T, 1, false, NW>(j, blk, sums);
+}
+// The same in the room that dX's product leaves on its SMs (11776 registers, 24 KB), which it begins beside:
+// dY was ready before that did.  Its last CTA waits for that product, so that whoever waits for this kernel has
+// waited for both.
+constexpr int kBesideWarps = 4;
+template <typename T>
+__global__ void __launch_bounds__(kBesideWarps * 32, 7) mx4_bias_kernel(const __grid_constant__ BiasJob bias) {
+  __shared__ float sums[kBesideWarps][32 * 8];
+  ptx::griddep_launch_dependents();
+  bias_block<T, kBesideWarps>(bias, blockIdx.x, sums);
+  if (blockIdx.x == gridDim.x - 1) ptx::griddep_wait();
 }
 
 template <typename T>
@@ -518,12 +539,7 @@ __global__ void __launch_bounds__(256, 4)  // the most demanding job must not co
   ptx::griddep_launch_dependents();
   int64_t blk = blockIdx.x;
   if (blk < bias.blocks) {
-    if (bias.cols * sizeof(T) % 16 == 0)
-      bias_part<T, 16 / sizeof(T), true>(bias, blk, sums);
-    else if (bias.lane == 8)
-      bias_part<T, 8, false>(bias, blk, sums);
-    else
-      bias_part<T, 1, false>(bias, blk, sums);
+    bias_block<T, 8>(bias, blk, sums);
     return;
   }
   blk -= bias.blocks;
@@ -837,14 +853,19 @@ cudaError_t mx4_gemm_bwd(const void* dY, const Mx4View& x, const Mx4View& w, con
   StageJob sj;
   const Operand a = staged(dY, d, d.out, base + l.dy, &sj);
   if (dX == nullptr && dW == nullptr) sj.blocks = 0;
+  const int es = d.dtype == MONARCH_BF16 ? 2 : 4;
   BiasJob bj = {};
   if (dbias != nullptr) {
-    const int es = d.dtype == MONARCH_BF16 ? 2 : 4;
     const int lane = n_out * es % 16 == 0 ? 16 / es : bias_parts(d) * ((n_out + 255) / 256) >= 2 * num_sms() ? 8 : 1;
     bj = BiasJob{dY, (float*)(base + l.bias), dbias, d.rows, n_out, lane, (int)((n_out + 32 * lane - 1) / (32 * lane)), bias_parts(d), 0};
     bj.blocks = bj.nparts * bj.cgroups;
   }
-  cudaError_t e = prepare(d, bj, dX != nullptr ? expand_job(w, base + l.w) : ExpandJob{}, dW != nullptr ? expand_job(x, base + l.x) : ExpandJob{},
+  // dbias beside dX's product, if that lasts as long as a pass over dY in the room it leaves: by the operations on
+  // a byte of dY.  us with dbias in the first launch and beside: 8192 x 1024 -> 4096 118.5 and 112.2, 2048 rows of
+  // eight 384 -> 512 blocks 35.8 and 33.2, of four 256 -> 1024 65.9 and 68.5 (8192 rows; in fp32, 1500: 53.2 and 50.9).
+  const bool apart = dbias != nullptr && dX != nullptr && dW != nullptr && d.rows * n_out * es >= 1 << 20 &&
+                     d.in * parts_of(d.dtype) >= 192 * es;
+  cudaError_t e = prepare(d, apart ? BiasJob{} : bj, dX != nullptr ? expand_job(w, base + l.w) : ExpandJob{}, dW != nullptr ? expand_job(x, base + l.x) : ExpandJob{},
                           sj, st);
   if (e != cudaSuccess) return e;
   SumJob sum_x = {}, sum_w = {}, sum_b = {};
@@ -855,9 +876,15 @@ cudaError_t mx4_gemm_bwd(const void* dY, const Mx4View& x, const Mx4View& w, con
     if (e != cudaSuccess) return e;
     if (p.nsplit > 1) sum_x = SumJob{part_x, dX, d.rows * n_in, p.nsplit, nullptr, 1};
   }
+  if (apart) {
+    const dim3 grid((unsigned)bj.blocks), block(kBesideWarps * 32);
+    e = d.dtype == MONARCH_BF16 ? launch_kernel(mx4_bias_kernel<__nv_bfloat16>, grid, block, 0, st, true, bj)
+                                : launch_kernel(mx4_bias_kernel<float>, grid, block, 0, st, true, bj);
+    if (e != cudaSuccess) return e;
+  }
   if (dW != nullptr) {
     const Plan p = dw_plan(d);
-    // beside dX's product, if that went before: its operands were ready when that began
+    // beside dX's product, if that went before (and dbias): its operands were ready when that began
     e = product<true, true>(rows_as_k(a, d, d.out), expanded(base + l.x, d.x()), Result{dW, d.out, d.in, d.nb, d.in, (int64_t)d.out * d.in, 0},
                             nullptr, d, d.rows, p, part_w, n_out * d.in, dX != nullptr, status, st);
     if (e != cudaSuccess) return e;

@@ -188,6 +188,29 @@ def test_linear_backward(rows, nb, inn, out, bias, dtype):
     assert dX is None and torch.equal(dW, got[1])
 
 
+# dbias beside dX's product: aligned rows, odd ones, fp32 parts; in a stream of calls that share a workspace, and replayed
+@pytest.mark.parametrize("rows,nb,inn,out,dtype", [
+    (1300, 1, 512, 1000, "bf16"), (900, 3, 384, 333, "bf16"), (1025, 1, 1024, 1100, "bf16"), (600, 2, 256, 501, "f32")])
+def test_linear_backward_of_a_long_batch(rows, nb, inn, out, dtype):
+    test_linear_backward(rows, nb, inn, out, True, dtype)
+    t, _ = layer(rows, nb, inn, out, True, dtype, seed=3)
+    Wq, Xq = bdl.mx4_quantise(t["W"]), bdl.mx4_quantise(t["X"], nblocks=nb)
+    steps = [t["dY"] * k for k in (1, -2, 0.5, 4)]  # exact multiples: so are the results
+    first = bdl.mx4_linear_bwd(steps[0], Xq, Wq, bias=True)
+    ws = torch.empty(bdl.mx4_linear_workspace_bytes(rows, nb, inn, out, dtype, bias=True, backward=True), dtype=torch.uint8, device="cuda")
+    given = torch.empty_like(steps[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept = bdl.mx4_linear_bwd(given, Xq, Wq, bias=True, workspace=ws)
+    for _ in range(3):
+        outs = [bdl.mx4_linear_bwd(d, Xq, Wq, bias=True, workspace=ws) for d in steps]
+        for d, o, k in zip(steps, outs, (1, -2, 0.5, 4)):
+            given.copy_(d)
+            graph.replay()
+            assert all(torch.equal(a, b * k) and torch.equal(c, a) for a, b, c in zip(o, first, kept))
+    assert bdl.last_device_status() == 0
+
+
 def test_backward_against_differences():
     """A step in one coordinate of an fp32 operand, big enough to move its quantised value, moves
     sum(Y * dY) by the gradient times that value's move (the layer is linear in each operand)."""
