@@ -188,6 +188,15 @@ def test_linear_backward(rows, nb, inn, out, bias, dtype):
     assert dX is None and torch.equal(dW, got[1])
 
 
+# few tokens, small weights: fewer tiles than warps, blocks in their place, shares of one to four scale tiles
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,nb,inn,out,bias", [
+    (12, 20, 70, 5, True), (30, 9, 300, 24, True), (20, 1, 1500, 64, False), (31, 1, 2048, 40, True), (9, 65, 128, 17, True),
+    (32, 3, 33, 128, True), (17, 2, 1030, 16, False), (25, 7, 513, 100, True), (8, 1, 4096, 3, True)])
+def test_linear_forward_of_few_tokens(rows, nb, inn, out, bias, dtype):
+    test_linear_forward_weights_only(rows, nb, inn, out, bias, dtype)
+
+
 # dbias beside dX's product: aligned rows, odd ones, fp32 parts; in a stream of calls that share a workspace, and replayed
 @pytest.mark.parametrize("rows,nb,inn,out,dtype", [
     (1300, 1, 512, 1000, "bf16"), (900, 3, 384, 333, "bf16"), (1025, 1, 1024, 1100, "bf16"), (600, 2, 256, 501, "f32")])
@@ -288,7 +297,8 @@ MONARCH = [  # (rows, nb1, in1, out1, nb2, in2, out2, out_transpose)
     (32, 32, 32, 32, 32, 32, 32, 1), (33, 16, 48, 48, 48, 16, 64, 1), (7, 4, 250, 250, 4, 250, 1000, 0),
     (5, 3, 10, 8, 4, 6, 5, 1), (2, 1, 40, 24, 2, 12, 9, 0), (9, 2, 300, 129, 6, 43, 17, 1), (12, 5, 33, 70, 7, 50, 21, 0),
     (3, 2, 2048, 1100, 2, 1100, 1030, 0), (20, 8, 640, 640, 8, 640, 1024, 1), (64, 4, 256, 64, 4, 64, 64, 0), (65, 8, 64, 64, 8, 64, 128, 0),
-    (200, 32, 32, 32, 32, 32, 32, 1), (300, 4, 256, 256, 4, 256, 1024, 0)]
+    (200, 32, 32, 32, 32, 32, 32, 1), (300, 4, 256, 256, 4, 256, 1024, 0), (17, 13, 40, 26, 13, 26, 9, 1),
+    (33, 52, 52, 52, 52, 52, 52, 1), (10, 9, 100, 33, 27, 11, 6, 1), (64, 64, 64, 64, 64, 64, 64, 1)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -494,3 +504,37 @@ def test_a_copied_weight_outlives_the_first():
     Wq.codes.zero_()
     assert torch.equal(bdl.mx4_linear_fwd(t["X"], twin), want)
     check_forward(want, v["x"], v, 96, "bf16", "Y")
+
+
+def test_two_threads_on_their_own_streams():
+    import threading
+    t, _ = layer(700, 2, 400, 512, True, "bf16")
+    Wq = bdl.mx4_quantise(t["W"])
+    shape = dict(nb1=16, in1=16, out1=16, nb2=16, in2=16, out2=16, out_transpose=1)
+    Rq = bdl.mx4_quantise(torch.randn(16, 16, 16, device="cuda").bfloat16())
+
+    def work(k):
+        X, dY = t["X"] * 2.0 ** k, t["dY"] * 2.0 ** -k
+        Xq = bdl.mx4_quantise(X, nblocks=2)
+        return [bdl.mx4_linear_fwd(Xq, Wq, bias=t["b"]), bdl.mx4_linear_fwd(X, Wq), bdl.mx4_linear_fwd(X[:1 + k], Wq, bias=t["b"]),
+                *bdl.mx4_linear_bwd(dY, Xq, Wq, bias=True), bdl.mx4_fwd(X[:3, :256].contiguous(), Rq, Rq, shape)]
+    want = [work(k) for k in range(2)]
+    torch.cuda.synchronize()
+    faults = []
+
+    def run(k):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(30):
+                    got = work(k)
+                    if not all(torch.equal(a, b) for a, b in zip(got, want[k])):
+                        faults.append(k)
+        except Exception as e:  # noqa: BLE001 - reported below
+            faults.append(e)
+    threads = [threading.Thread(target=run, args=(k,)) for k in range(2)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    torch.cuda.synchronize()
+    assert not faults and bdl.last_device_status() == 0
