@@ -41,7 +41,8 @@ struct GJob {
   int nk, parts;       // K stages of one part; parts of A
   int stages_per_split;
   int beside;          // run beside the kernel that was launched just before (see the kernel)
-  int a_chunked, b_chunked;  // inner index M / N: the map is 4-D and both 64-wide chunks are one box
+  int a_chunks, b_chunks;  // inner index M / N: copies a stage takes (see load_operand)
+  int a_bytes, b_bytes;    // of a CTA's stage
 };
 
 template <bool PAIR_, bool A_MN_, bool B_MN_, typename T_, bool TMA_OUT_>
@@ -98,20 +99,21 @@ __device__ __forceinline__ void load3(void* dst, const CUtensorMap* m, uint64_t*
     ptx::tma_load_3d(dst, m, bar, x, y, z, pol);
 }
 // 128 rows (M or N index r0 ..) x 64 of K (index k0 ..) of one operand.  MN: the inner index of the map is
-// the operand's row.  b_k: the batch coordinate, which for an MN operand may also hold the part.
+// the operand's row, and `chunks` says how its two 64-wide halves come: 0: in one box of a 4-D map, 1: the first
+// alone, 2: one after the other.  b_k: the batch coordinate, which for an MN operand may also hold the part.
 template <bool PAIR, bool MN>
-__device__ __forceinline__ void load_operand(uint8_t* dst, const CUtensorMap* m, int chunked, uint64_t* bar, uint32_t bar0,
+__device__ __forceinline__ void load_operand(uint8_t* dst, const CUtensorMap* m, int chunks, uint64_t* bar, uint32_t bar0,
                                              int r0, int k0, int b_k, uint64_t pol) {
   if (!MN) {
     load3<PAIR>(dst, m, bar, bar0, k0, r0, b_k, pol);
-  } else if (chunked) {
+  } else if (chunks == 0) {
     if (PAIR)
       ptx::tma_load_4d_pair(dst, m, bar0, 0, k0, r0 / 64, b_k, pol);
     else
       ptx::tma_load_4d(dst, m, bar, 0, k0, r0 / 64, b_k, pol);
   } else {
     load3<PAIR>(dst, m, bar, bar0, r0, k0, b_k, pol);
-    load3<PAIR>(dst + 8192, m, bar, bar0, r0 + 64, k0, b_k, pol);
+    if (chunks == 2) load3<PAIR>(dst + 8192, m, bar, bar0, r0 + 64, k0, b_k, pol);
   }
 }
 
@@ -185,14 +187,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int st = it % C::NSTAGE;
           if (!wait_or_abort(&bars->empty[st], ((it / C::NSTAGE) & 1) ^ 1, abort_flag, status)) { ok = false; break; }
           uint8_t* sa = ring + st * C::STAGE;
-          if (first) ptx::mbar_arrive_expect_tx(&bars->full[st], (PAIR ? 2 : 1) * C::STAGE);
+          if (first) ptx::mbar_arrive_expect_tx(&bars->full[st], (PAIR ? 2 : 1) * (job.a_bytes + job.b_bytes));
           const uint32_t fb = full0 + (uint32_t)(st * sizeof(uint64_t));
           const int part = kb / job.nk, k0 = (kb - part * job.nk) * 64;
           if (C::A_MN)
-            load_operand<PAIR, true>(sa, &tmA, job.a_chunked, &bars->full[st], fb, m0, k0, c.b * job.parts + part, pol);
+            load_operand<PAIR, true>(sa, &tmA, job.a_chunks, &bars->full[st], fb, m0, k0, c.b * job.parts + part, pol);
           else
             load_operand<PAIR, false>(sa, &tmA, 0, &bars->full[st], fb, m0, kb * 64, c.b, pol);
-          load_operand<PAIR, C::B_MN>(sa + C::A_BYTES, &tmB, job.b_chunked, &bars->full[st], fb, n0, k0, c.b, pol);
+          load_operand<PAIR, C::B_MN>(sa + C::A_BYTES, &tmB, job.b_chunks, &bars->full[st], fb, n0, k0, c.b, pol);
         }
       }
       if (!PAIR) {  // no copy may still be in flight when the CTA leaves (a pair's MMAs wait for theirs)
@@ -604,15 +606,22 @@ struct Operand {
   int64_t inner, outer, batch;
   int64_t s_outer, s_batch;
 };
-bool kmajor_map(CUtensorMap* m, const Operand& o) {
+// M (or N) index outside.  A box is no longer than the `extent` rows of the operand, if it is alone (rows behind the
+// last are dear to TMA: 2000 rows of two 2048 -> 16 blocks forward 10.4 us and 9.4 so, dW 23.4 and 13.7 with half of
+// its tile); what stands behind belongs to results that are not stored.
+bool kmajor_map(CUtensorMap* m, const Operand& o, int64_t extent, bool alone, int* bytes) {
+  const int rows = alone && extent < 128 ? (int)((extent + 7) / 8 * 8) : 128;
+  *bytes = rows * 128;
   const cuuint64_t dims[3] = {(cuuint64_t)o.inner, (cuuint64_t)o.outer, (cuuint64_t)o.batch};
   const cuuint64_t st[2] = {(cuuint64_t)o.s_outer * 2, (cuuint64_t)o.s_batch * 2};
-  const cuuint32_t box[3] = {64, 128, 1};
+  const cuuint32_t box[3] = {64, (cuuint32_t)rows, 1};
   return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, o.p, dims, st, box);
 }
-bool mnmajor_map(CUtensorMap* m, const Operand& o, int* chunked) {
-  *chunked = o.inner % 64 == 0;
-  if (*chunked) {
+bool mnmajor_map(CUtensorMap* m, const Operand& o, int64_t extent, bool alone, int* bytes, int* chunks) {
+  const bool half = alone && extent <= 64;
+  *bytes = half ? 8192 : 16384;
+  *chunks = half ? 1 : o.inner % 64 == 0 ? 0 : 2;
+  if (*chunks == 0) {
     const cuuint64_t dims[4] = {64, (cuuint64_t)o.outer, (cuuint64_t)o.inner / 64, (cuuint64_t)o.batch};
     const cuuint64_t st[3] = {(cuuint64_t)o.s_outer * 2, 128, (cuuint64_t)o.s_batch * 2};
     const cuuint32_t box[4] = {64, 64, 2, 1};
@@ -665,9 +674,9 @@ template <class C>
 cudaError_t launch(const Operand& a, const Operand& b, const Result& d, const void* bias, GJob j, int* status, cudaStream_t st) {
   using T = typename C::T;
   CUtensorMap mA, mB, mD;
-  j.a_chunked = j.b_chunked = 0;
-  if (!(C::A_MN ? mnmajor_map(&mA, a, &j.a_chunked) : kmajor_map(&mA, a)) ||
-      !(C::B_MN ? mnmajor_map(&mB, b, &j.b_chunked) : kmajor_map(&mB, b)))
+  constexpr bool alone = !C::PAIR;  // a pair's two CTAs hold different rows
+  if (!(C::A_MN ? mnmajor_map(&mA, a, d.m, alone, &j.a_bytes, &j.a_chunks) : kmajor_map(&mA, a, d.m, alone, &j.a_bytes)) ||
+      !(C::B_MN ? mnmajor_map(&mB, b, d.n, alone, &j.b_bytes, &j.b_chunks) : kmajor_map(&mB, b, d.n, alone, &j.b_bytes)))
     return cudaErrorInvalidValue;
   if (C::TMA_OUT) {
     const cuuint64_t dims[4] = {(cuuint64_t)d.n, (cuuint64_t)d.nb, (cuuint64_t)d.m, (cuuint64_t)j.nsplit};
