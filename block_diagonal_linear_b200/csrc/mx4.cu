@@ -74,9 +74,14 @@ int status_of(cudaError_t e) { return e == cudaSuccess ? MONARCH_OK : MONARCH_ER
 // beyond them the weight is expanded for the bf16 products.  Both measured, 4096 -> 4096 and four 250 -> 1000 blocks:
 // bf16 64 rows 21.4 and 8.2 us against 20.7 and 6.6 in two launches; fp32 32 rows 20.6 and 7.0, 64 rows 57.6 and 9.5
 // against 30.5 and 9.4.
-int64_t few_rows(int dtype) { return dtype == MONARCH_BF16 ? 64 : 32; }
+// So do more rows of a small weight, for which two launches are the greater cost: 300 rows of four 256 -> 256 blocks 6.2
+// and 6.5, 1000 of 512 -> 128 5.0 and 7.4, 128 of sixty-four 64 -> 64 blocks 5.4 and 5.1; fp32 128 of four 256 -> 256 5.9
+// and 9.8, 100 of sixty-four 64 -> 64 7.4 and 6.8.
+bool few_rows(const Mx4Linear& d) {
+  return d.rows <= (d.dtype == MONARCH_BF16 ? 64 : 32) || mx4_rows_little(d.w(), d.rows, d.dtype == MONARCH_BF16 ? 1 : 3);
+}
 
-size_t wfwd_workspace(const Mx4Linear& d) { return d.rows <= few_rows(d.dtype) ? 0 : mx4_gemm_fwd_bytes(d); }
+size_t wfwd_workspace(const Mx4Linear& d) { return few_rows(d) ? 0 : mx4_gemm_fwd_bytes(d); }
 size_t bwd_workspace(const Mx4Linear& d) { return d.rows == 0 ? 0 : mx4_gemm_bwd_bytes(d); }
 
 Mx4Shape r_shape(const monarch_dims& d) { return Mx4Shape{d.out1, d.nb1, d.in1}; }
@@ -89,13 +94,20 @@ int check_monarch(const monarch_dims* d) {
   return check_size(d->out2, d->nb2, d->in2, d->dtype);
 }
 
-// Up to this many rows the Monarch map is two products with the middle vector in fp32 in the
-// workspace; longer batches expand the factors there and run the plain forward.
-constexpr int64_t kMonarchFewRows = 64;
+// Whether the Monarch map is two products by the few-rows kernels, with the middle vector in fp32 in the workspace;
+// else the factors are expanded there and the plain forward runs.  us, both ways: 200 rows of n = 4096 18.8 and 23.0,
+// 400 33 and 25; 400 of n = 1024 10.1 and 16.5, 1000 20.7 and 17.0; four 256 -> 256 -> 1024 blocks, 100 rows 16 and 33,
+// 400 50 and 36.  The plain forward's generic kernels are slower at any number (1000 rows of four 256 -> 256 -> 256
+// blocks 44 and 461).
+bool few_rows(const monarch_dims& d) {
+  if (d.rows <= 64) return true;
+  if (d.rows > kRowsMost) return false;
+  return mx4_rows_work(r_shape(d), d.rows) + mx4_rows_work(l_shape(d), d.rows) <= 13000 || monarch_fwd_path(&d) == 0;
+}
 
 size_t monarch_workspace(const monarch_dims& d) {
   const Shape s = to_shape(d);
-  if (s.rows <= kMonarchFewRows) return al256((size_t)(s.rows * s.n_mid() * 4));
+  if (few_rows(d)) return al256((size_t)(s.rows * s.n_mid() * 4));
   const int64_t es = elem_bytes(d.dtype);
   return al256((size_t)(s.n_R() * es)) + al256((size_t)(s.n_L() * es));
 }
@@ -186,7 +198,7 @@ int monarch_mx4_linear_wfwd(const void* X, const void* w_codes, const void* w_sc
   const Mx4View w{(const uint8_t*)w_codes, (const uint8_t*)w_scales, ws};
   const void* b = d.has_bias ? bias : nullptr;
   cudaStream_t st = (cudaStream_t)stream;
-  if (d.rows <= few_rows(d.dtype))
+  if (few_rows(d))
     return status_of(mx4_rows_fwd(X, d.dtype, w, b, d.rows, Mx4Out::blocks(d.nb, d.out), Y, d.dtype, false, st));
   int* status = status_ptr();
   if (status == nullptr) return MONARCH_ERR_CUDA;
@@ -246,7 +258,7 @@ int monarch_mx4_fwd(const void* X, const void* r_codes, const void* r_scales, co
     return rc;
   const Mx4View r{(const uint8_t*)r_codes, (const uint8_t*)r_scales, rs}, l{(const uint8_t*)l_codes, (const uint8_t*)l_scales, ls};
   cudaStream_t st = (cudaStream_t)stream;
-  if (s.rows <= kMonarchFewRows) {
+  if (few_rows(*d)) {
     // U = blockdiag(R) X, written through P, then blockdiag(L) of contiguous slices, through P_out.  The
     // second kernel may ask for L at once: whatever wrote it had ended when the first began.
     if (mx4_rows_fwd(X, d->dtype, r, nullptr, s.rows, Mx4Out::transposed(s.nb1, s.out1), workspace, MONARCH_F32, false, st) !=

@@ -230,6 +230,11 @@ struct Mx4Linear {
 // Both operands in MX4 on the block-scaled tensor cores, every size and both types (mx4_tc.cu).
 cudaError_t mx4_tc_fwd(const Mx4View& x, const Mx4View& w, const void* bias, const Mx4Linear& d, void* Y, int* status,
                        cudaStream_t st);
+// What the direct few-rows kernel does, in products of 16 outputs, 128 inputs and 8 tokens, and whether that is little
+// (6 us or so) where X comes in `parts` bf16 parts.
+double mx4_rows_work(const Mx4Shape& w, int64_t rows);
+bool mx4_rows_little(const Mx4Shape& w, int64_t rows, int parts);
+constexpr int64_t kRowsMost = 8 * 65535;  // rows that the few-rows kernels take
 // X as it is, few rows (mx4_rows.cu); X, Y fp32 or bf16.  w_early: no kernel of the stream that may still
 // run writes the weight, so it may be read ahead of the grid-dependency wait.
 cudaError_t mx4_rows_fwd(const void* X, int x_dtype, const Mx4View& w, const void* bias, int64_t rows, const Mx4Out& o, void* Y,

@@ -420,12 +420,11 @@ cudaError_t launch_batch(const void* X, const Mx4View& w, const void* bias, int6
 template <typename TX, int PARTS, typename TY, bool VEC>
 cudaError_t launch_vec(const void* X, const Mx4View& w, const void* bias, int64_t rows, const Mx4Out& o, void* Y, bool w_early,
                        cudaStream_t st) {
-  // The direct kernel, as long as cutting inputs and expanding codes again and again is little work: every 8 tokens
-  // do it for every 16 outputs.  us, direct and batch: 32 bf16 tokens of sixty-four 64 -> 64 blocks 2.2 and 4.1, of
-  // 1024 -> 1024 2.6 and 5.3, of 1024 -> 4096 7.9 and 7.2, of 4096 -> 4096 16.5 and 12.2; 33 of four 250 -> 1000 blocks
-  // 5.7 and 6.9; 16 fp32 tokens of 1024 -> 1024 3.8 and 5.2, of 1024 -> 4096 10.1 and 6.9
-  const int64_t work = (int64_t)w.s.nblocks * w.s.rows * w.s.cols * ((rows + 7) / 8) * PARTS;
-  if ((PARTS == 1 && rows <= 8) || work <= (VEC ? 10 << 20 : 6 << 20))
+  // The direct kernel for short inputs, and as long as cutting inputs and expanding codes for every 16 outputs of every
+  // 8 tokens is little work.  us, direct and batch: 32 bf16 tokens of sixty-four 64 -> 64 blocks 2.2 and 4.1, 64 of
+  // 256 -> 4096 4.9 and 6.9, 32 of 1024 -> 1024 2.6 and 5.3, of 1024 -> 4096 7.9 and 7.2, of 4096 -> 4096 16.5 and 12.2; 16
+  // fp32 tokens of 1024 -> 1024 3.8 and 5.2, of 1024 -> 4096 10.1 and 6.9
+  if ((PARTS == 1 && rows <= 8) || w.s.katoms() <= 2 || mx4_rows_little(w.s, rows, PARTS))
     return launch_token<TX, PARTS, TY, VEC>(X, w, bias, rows, o, Y, w_early, st);
   if constexpr (PARTS > 1) {
     if (rows <= 8) return launch_batch<TX, PARTS, TY, VEC, 1>(X, w, bias, rows, o, Y, w_early, st);
@@ -446,6 +445,13 @@ cudaError_t launch_rows(const void* X, const Mx4View& w, const void* bias, int64
 }
 
 }  // namespace
+
+double mx4_rows_work(const Mx4Shape& w, int64_t rows) {
+  return (double)w.nblocks * (double)((w.rows + 15) / 16) * w.katoms() * (double)((rows + 7) / 8);
+}
+bool mx4_rows_little(const Mx4Shape& w, int64_t rows, int parts) {
+  return mx4_rows_work(w, rows) <= (parts == 1 ? 5120 : parts == 2 ? 4096 : 3072);
+}
 
 cudaError_t mx4_rows_fwd(const void* X, int x_dtype, const Mx4View& w, const void* bias, int64_t rows, const Mx4Out& o, void* Y,
                          int y_dtype, bool w_early, cudaStream_t st) {

@@ -382,8 +382,8 @@ typedef struct {
 } monarch_mx4_linear_dims;
 
 /* Workspace of monarch_mx4_linear_wfwd and of monarch_mx4_linear_bwd, 256-byte aligned (0: may be NULL; 0
- * if ld is bad).  It holds the MX4 operands' values in bf16 (forward: beyond 64 bf16 or 32 fp32 rows), plain
- * operands whose rows TMA cannot address, and partial sums. */
+ * if ld is bad).  It holds the MX4 operands' values in bf16, plain operands whose rows TMA cannot address, and
+ * partial sums.  The forward needs none up to 64 bf16 or 32 fp32 rows, nor for more of a small weight. */
 MONARCH_API size_t monarch_mx4_linear_wfwd_workspace_bytes(const monarch_mx4_linear_dims* ld);
 MONARCH_API size_t monarch_mx4_linear_bwd_workspace_bytes(const monarch_mx4_linear_dims* ld);
 /* Both operands in MX4. */
@@ -406,8 +406,10 @@ MONARCH_API int monarch_mx4_linear_bwd(const void* dY, const void* x_codes, cons
                                        void* dbias, void* workspace, size_t workspace_bytes, void* stream);
 
 /* monarch_fwd with both factors in MX4: R as (nb1, out1, in1), L as (nb2, out2, in2), quantised by block.
- * X and Y have d->dtype.  Up to 64 rows (decoding) the middle vector stays in fp32; longer batches run
- * monarch_fwd's kernels on the factors' values, with its rounding of the middle vector.  workspace: >= monarch_mx4_fwd_workspace_bytes(d), 256-byte aligned. */
+ * X and Y have d->dtype.  Up to 64 rows (decoding), for longer batches through small factors and where
+ * monarch_fwd_path is 0 the middle vector stays in fp32; other calls run monarch_fwd's kernels on the
+ * factors' values, with its rounding of the middle vector.
+ * workspace: >= monarch_mx4_fwd_workspace_bytes(d), 256-byte aligned. */
 MONARCH_API size_t monarch_mx4_fwd_workspace_bytes(const monarch_dims* d);
 MONARCH_API int monarch_mx4_fwd(const void* X, const void* r_codes, const void* r_scales, const void* l_codes,
                                 const void* l_scales, const monarch_dims* d, void* Y, void* workspace,

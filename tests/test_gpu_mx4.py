@@ -188,6 +188,15 @@ def test_linear_backward(rows, nb, inn, out, bias, dtype):
     assert dX is None and torch.equal(dW, got[1])
 
 
+# long prompts: the weight expanded, X in place or staged, K split or not
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,nb,inn,out,bias", [
+    (900, 2, 333, 500, True), (1500, 3, 200, 129, False), (2000, 1, 100, 700, True), (1100, 1, 1000, 72, True), (600, 2, 250, 1000, True),
+    (70, 3, 1100, 900, False), (400, 1, 3000, 100, True)])
+def test_linear_forward_of_a_prompt(rows, nb, inn, out, bias, dtype):
+    test_linear_forward_weights_only(rows, nb, inn, out, bias, dtype)
+
+
 # few tokens, small weights: fewer tiles than warps, blocks in their place, shares of one to four scale tiles
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("rows,nb,inn,out,bias", [
@@ -298,7 +307,8 @@ MONARCH = [  # (rows, nb1, in1, out1, nb2, in2, out2, out_transpose)
     (5, 3, 10, 8, 4, 6, 5, 1), (2, 1, 40, 24, 2, 12, 9, 0), (9, 2, 300, 129, 6, 43, 17, 1), (12, 5, 33, 70, 7, 50, 21, 0),
     (3, 2, 2048, 1100, 2, 1100, 1030, 0), (20, 8, 640, 640, 8, 640, 1024, 1), (64, 4, 256, 64, 4, 64, 64, 0), (65, 8, 64, 64, 8, 64, 128, 0),
     (200, 32, 32, 32, 32, 32, 32, 1), (300, 4, 256, 256, 4, 256, 1024, 0), (17, 13, 40, 26, 13, 26, 9, 1),
-    (33, 52, 52, 52, 52, 52, 52, 1), (10, 9, 100, 33, 27, 11, 6, 1), (64, 64, 64, 64, 64, 64, 64, 1)]
+    (33, 52, 52, 52, 52, 52, 52, 1), (300, 4, 256, 256, 4, 256, 256, 0), (600, 3, 10, 8, 4, 6, 5, 1), (500, 2, 300, 129, 6, 43, 17, 1),
+    (1200, 32, 32, 32, 32, 32, 32, 1), (10, 9, 100, 33, 27, 11, 6, 1), (64, 64, 64, 64, 64, 64, 64, 1)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])

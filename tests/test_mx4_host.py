@@ -136,7 +136,7 @@ def test_linear_refusals():
         assert g(good, Y=P((3 << 40) + 32)) == CODES["MONARCH_ERR_ALIAS"]      # W's codes
         assert g(good, Y=P((5 << 40) - 16)) == CODES["MONARCH_ERR_ALIAS"]      # into the bias
         assert g(D(0, 2, 64, 96, 1, 1), wc=None, ws=None, b=None, Y=None) == 0
-    long = D(65, 2, 64, 96, 1, bdl.MONARCH_BF16)   # beyond 64 rows the weight's values are expanded in a workspace
+    long = D(700, 2, 640, 960, 1, bdl.MONARCH_BF16)   # many rows of a large weight: its values are expanded in a workspace
     need = L.monarch_mx4_linear_wfwd_workspace_bytes(ctypes.byref(long))
     assert need > 0 and L.monarch_mx4_linear_wfwd_workspace_bytes(ctypes.byref(good)) == 0
     assert w(long, work=None) == w(long, n=need - 1) == CODES["MONARCH_ERR_WORKSPACE"]
