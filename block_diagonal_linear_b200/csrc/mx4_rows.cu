@@ -12,10 +12,10 @@
 // up to four scale tiles of codes before it uses the first.  The inputs are split up to 8 ways, and the
 // shares' sums join in a fixed order.
 //
-// Up to 8 bf16 tokens, and more where the weight is small (mx4_token_kernel), the shares are warps of a CTA
-// and a lane reads its inputs where they are.  Warps that are left take further tiles, or neighbouring blocks: of
+// Up to 8 bf16 tokens, and more where inputs are short or the weight small (mx4_token_kernel), the shares are warps
+// of a CTA and a lane reads its inputs where they are.  Warps that are left take further tiles, or neighbouring blocks: of
 // a transposed result (a Monarch stage) these lie next to each other (32 tokens through sixty-four 64 x 64 blocks
-// twice: 5.1 us, 13.5 with a block a CTA).  With a large weight every warp would gather and cut its own inputs
+// twice: 5.5 us, 13.5 with a block a CTA).  With a large weight every warp would gather and cut its own inputs
 // too often (4096 -> 4096: 16.5 us for 32 bf16 tokens against 12.2, 12.2 for one in fp32 against 8.1); there
 // (mx4_batch_kernel, up to 64 tokens a pass) the shares are CTAs of a cluster, and a CTA's 8 warps take 128 outputs
 // and share one copy of the inputs in shared memory, already cut into parts, in the order in which lanes read it.
