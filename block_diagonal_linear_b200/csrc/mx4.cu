@@ -173,6 +173,8 @@ int monarch_mx4_linear_fwd(const void* x_codes, const void* x_scales, const void
                          Range(w_scales, ws.scale_bytes()), Range(d.has_bias ? bias : nullptr, n_out * es)})) != MONARCH_OK)
     return rc;
   const Mx4View x{(const uint8_t*)x_codes, (const uint8_t*)x_scales, xs}, w{(const uint8_t*)w_codes, (const uint8_t*)w_scales, ws};
+  if (mx4_rows_quantised(ws, d.rows))
+    return status_of(mx4_rows_fwd(x, w, d.has_bias ? bias : nullptr, Mx4Out::blocks(d.nb, d.out), Y, d.dtype, (cudaStream_t)stream));
   int* status = status_ptr();
   if (status == nullptr) return MONARCH_ERR_CUDA;
   return status_of(mx4_tc_fwd(x, w, d.has_bias ? bias : nullptr, d, Y, status, (cudaStream_t)stream));

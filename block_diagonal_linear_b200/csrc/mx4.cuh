@@ -239,6 +239,9 @@ constexpr int64_t kRowsMost = 8 * 65535;  // rows that the few-rows kernels take
 // run writes the weight, so it may be read ahead of the grid-dependency wait.
 cudaError_t mx4_rows_fwd(const void* X, int x_dtype, const Mx4View& w, const void* bias, int64_t rows, const Mx4Out& o, void* Y,
                          int y_dtype, bool w_early, cudaStream_t st);
+// The same with X in MX4, and whether that is quicker than the tensor-core kernel for both operands in MX4.
+bool mx4_rows_quantised(const Mx4Shape& w, int64_t rows);
+cudaError_t mx4_rows_fwd(const Mx4View& x, const Mx4View& w, const void* bias, const Mx4Out& o, void* Y, int y_dtype, cudaStream_t st);
 // Products with a plain operand on the bf16 tensor cores, every size and both types (mx4_gemm.cu); ws: the
 // bytes that the size query gives.  dX, dW and dbias may be NULL.
 size_t mx4_gemm_fwd_bytes(const Mx4Linear& d);

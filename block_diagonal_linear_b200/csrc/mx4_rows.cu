@@ -1,10 +1,11 @@
-// Few tokens through an MX4 weight:  Y(r; b, o) = sum_i X[r][b*in + i] W^[b][o][i] (+ bias), X as it is.
+// Few tokens through an MX4 weight:  Y(r; b, o) = sum_i X[r][b*in + i] W^[b][o][i] (+ bias), X as it is or in MX4.
 //
 // A decoding step reads the whole weight for a handful of tokens, so the kernels are bound by the
 // latency and bandwidth of that one read (17/32 bytes a weight).  The product runs on mma.sync
 // m16n8k16 with the weights as the 16-row operand and 8 tokens as the columns: codes become bf16
 // values in registers (exact), X enters as one bf16 part, or, in fp32, as 2 or 3 parts that are cut
-// off one after another (3 parts hold all 24 bits; 2 leave 2^-16, below a bf16 result's half step).
+// off one after another (3 parts hold all 24 bits; 2 leave 2^-16, below a bf16 result's half step); an MX4 X
+// becomes bf16 values as the weight does.
 //
 // A warp takes 16 outputs and walks scale tiles of 128 inputs: a lane holds one whole scale block of
 // two outputs (16 bytes of codes each), so that one multiplier serves all of a lane's values; which
@@ -19,6 +20,8 @@
 // too often (4096 -> 4096: 16.5 us for 32 bf16 tokens against 12.2, 12.2 for one in fp32 against 8.1); there
 // (mx4_batch_kernel, up to 64 tokens a pass) the shares are CTAs of a cluster, and a CTA's 8 warps take 128 outputs
 // and share one copy of the inputs in shared memory, already cut into parts, in the order in which lanes read it.
+#include <type_traits>
+
 #include "mx4.cuh"
 #include "tc_common.cuh"
 
@@ -142,20 +145,37 @@ __device__ __forceinline__ void values(const Codes& c, int t, uint32_t (&a0)[16]
     }
   }
 }
+// The same for the 32 codes of one token's scale block.
+__device__ __forceinline__ void values(uint4 q, uint32_t e, uint32_t (&a)[16]) {
+  const uint32_t f = (e > 128u ? 253u : e + 126u) * 0x00800080u;
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    uint32_t p[4];
+    mx4::spread8(w[v], p);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) a[4 * v + j] = mul_bf16x2(p[j], f);
+  }
+  if (__any_sync(0xffffffffu, e > 128u)) {
+    const uint32_t h = e > 128u ? (e == 255u ? 0x7fc07fc0u : e * 0x00800080u) : 0x3f803f80u;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) a[j] = mul_bf16x2(a[j], h);
+  }
+}
 // acc += the 32 inputs' products of word v.  mma.sync cuts its sums off (2^-23 a step, always towards
-// zero): an fp32 result (3 parts) takes them in runs of 32 inputs and joins the runs with rounded
-// additions (4096 inputs: 1.3e-6 off without, 1e-7 with).
-template <int PARTS>
+// zero): an fp32 result takes them in runs of 32 inputs and joins the runs with rounded additions (4096 inputs:
+// 1.3e-6 off without, 1e-7 with).
+template <int PARTS, bool RUNS = PARTS == 3>
 __device__ __forceinline__ void product(float (&acc)[4], const uint32_t (&a0)[16], const uint32_t (&a1)[16], int v,
                                         const uint32_t (&bp)[PARTS][4]) {
   float run[4] = {};
-  float(&sum)[4] = PARTS == 3 ? run : acc;
+  float(&sum)[4] = RUNS ? run : acc;
 #pragma unroll
   for (int q = PARTS - 1; q >= 0; --q) {
     mma_16816(sum, a0[4 * v], a1[4 * v], a0[4 * v + 1], a1[4 * v + 1], bp[q][0], bp[q][1]);
     mma_16816(sum, a0[4 * v + 2], a1[4 * v + 2], a0[4 * v + 3], a1[4 * v + 3], bp[q][2], bp[q][3]);
   }
-  if (PARTS == 3) {
+  if (RUNS) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[e] += run[e];
   }
@@ -165,10 +185,14 @@ constexpr int kAhead = 4;  // scale tiles of codes in flight
 
 constexpr int kPlane = 16 * 9 + 4;  // a warp's sums, 16 outputs x 8 tokens: padded, 8 blocks x 4 outputs in 32 banks
 
+struct QuantisedX {};  // in place of X's type: X is an Mx4 view
+
 // Warps of a CTA: 2^lk shares of the inputs, 2^lb neighbouring blocks, `per` tiles of 16 outputs; 8 tokens.
 template <typename TX, int PARTS, typename TY, bool VEC, int AHEAD>
 __global__ void __launch_bounds__(kWarps * 32, 2)
-    mx4_token_kernel(const TX* X, Mx4View w, int64_t rows, Mx4Out o, const TY* bias, TY* Y, int lk, int lb, int per, bool w_early) {
+    mx4_token_kernel(const TX* X, Mx4View xq, Mx4View w, int64_t rows, Mx4Out o, const TY* bias, TY* Y, int lk, int lb, int per,
+                     bool w_early) {
+  constexpr bool QX = std::is_same<TX, QuantisedX>::value;
   __shared__ float part[kWarps * kPlane];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   const int wk = 1 << lk, nbw = 1 << lb;
@@ -178,7 +202,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   CodeRows cr(w, b, (tile0 + mw) * 16 + g, t);
   if (mw >= per) cr.katoms = 0;  // nothing to do but the join
   const int64_t pitch = (int64_t)w.s.nblocks * w.s.cols;
-  const TX *p = X + r * pitch + (int64_t)b * w.s.cols + t * 32, *end = X + rows * pitch;
+  const TX *p = QX ? nullptr : X + r * pitch + (int64_t)b * w.s.cols + t * 32, *end = QX ? nullptr : X + rows * pitch;
+  const uint8_t* xc = QX ? xq.codes + xq.s.code_row(b, r) + t * 16 : nullptr;
+  const uint8_t* xs = QX ? xq.scales + xq.s.scale_at(b, r, 0) + t : nullptr;
 
   float acc[4] = {};
   Codes c[AHEAD];
@@ -199,16 +225,33 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     for (int i = 0; i < AHEAD; ++i) {
       const int ka = ka0 + i * wk;
       if (ka >= cr.katoms) break;
-      uint32_t x[4][8], a0[16], a1[16];
+      uint32_t a0[16], a1[16];
+      if constexpr (QX) {  // a lane's 32 inputs are one scale block of its token
+        const bool live = r < rows && ka * 4 + t < cr.kblocks;
+        const uint4 q = live ? *(const uint4*)(xc + (int64_t)ka * 64) : make_uint4(0, 0, 0, 0);
+        const uint32_t byte = live ? xs[(int64_t)ka * 512] : 0u;
+        uint32_t x[16];
+        values(c[i], t, a0, a1);
+        if (AHEAD == 1) c[0] = cr.at(ka + wk);
+        values(q, byte, x);
 #pragma unroll
-      for (int v = 0; v < 4; ++v) load8<VEC>(p + ka * 128 + 8 * v, r < rows ? w.s.cols - ka * 128 - t * 32 - 8 * v : 0, end, x[v]);
-      values(c[i], t, a0, a1);
-      if (AHEAD == 1) c[0] = cr.at(ka + wk);
+        for (int v = 0; v < 4; ++v) {
+          const uint32_t bp[1][4] = {{x[4 * v], x[4 * v + 1], x[4 * v + 2], x[4 * v + 3]}};
+          product<1, sizeof(TY) == 4>(acc, a0, a1, v, bp);
+        }
+      } else {
+        uint32_t x[4][8];
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        uint32_t bp[PARTS][4];
-        split8<PARTS>(x[v], bp, (const TX*)nullptr);
-        product<PARTS>(acc, a0, a1, v, bp);
+        for (int v = 0; v < 4; ++v)
+          load8<VEC>(p + ka * 128 + 8 * v, r < rows ? w.s.cols - ka * 128 - t * 32 - 8 * v : 0, end, x[v]);
+        values(c[i], t, a0, a1);
+        if (AHEAD == 1) c[0] = cr.at(ka + wk);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          uint32_t bp[PARTS][4];
+          split8<PARTS>(x[v], bp, (const TX*)nullptr);
+          product<PARTS>(acc, a0, a1, v, bp);
+        }
       }
     }
   }
@@ -367,7 +410,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
 }
 
 template <typename TX, int PARTS, typename TY, bool VEC>
-cudaError_t launch_token(const void* X, const Mx4View& w, const void* bias, int64_t rows, const Mx4Out& o, void* Y, bool w_early,
+cudaError_t launch_token(const void* X, const Mx4View& xq, const Mx4View& w, const void* bias, int64_t rows, const Mx4Out& o, void* Y, bool w_early,
                          cudaStream_t st) {
   const int64_t mtiles = (w.s.rows + 15) / 16;
   int lk = 0, lb = 0;
@@ -380,10 +423,10 @@ cudaError_t launch_token(const void* X, const Mx4View& w, const void* bias, int6
   // shares of one or two scale tiles run quicker in less code (16 tokens of 1024 -> 1024: 2.1 us, 2.4 with four
   // tiles ahead), the longest want the loads (8 of 4096 -> 4096 in fp32: 15.2 us and 18.1 without)
   return w.s.katoms() <= 2 << lk
-             ? launch_kernel(mx4_token_kernel<TX, PARTS, TY, VEC, 1>, grid, block, 0, st, true, (const TX*)X, w, rows, o,
-                             (const TY*)bias, (TY*)Y, lk, lb, per, w_early)
-             : launch_kernel(mx4_token_kernel<TX, PARTS, TY, VEC, kAhead>, grid, block, 0, st, true, (const TX*)X, w, rows, o,
-                             (const TY*)bias, (TY*)Y, lk, lb, per, w_early);
+             ? launch_kernel(mx4_token_kernel<TX, PARTS, TY, VEC, 1>, grid, block, 0, st, true, (const TX*)X, xq, w, rows,
+                             o, (const TY*)bias, (TY*)Y, lk, lb, per, w_early)
+             : launch_kernel(mx4_token_kernel<TX, PARTS, TY, VEC, kAhead>, grid, block, 0, st, true, (const TX*)X, xq, w, rows,
+                             o, (const TY*)bias, (TY*)Y, lk, lb, per, w_early);
 }
 
 template <typename TX, int PARTS, typename TY, bool VEC, int NT>
@@ -425,7 +468,7 @@ cudaError_t launch_vec(const void* X, const Mx4View& w, const void* bias, int64_
   // 256 -> 4096 4.9 and 6.9, 32 of 1024 -> 1024 2.6 and 5.3, of 1024 -> 4096 7.9 and 7.2, of 4096 -> 4096 16.5 and 12.2; 16
   // fp32 tokens of 1024 -> 1024 3.8 and 5.2, of 1024 -> 4096 10.1 and 6.9
   if ((PARTS == 1 && rows <= 8) || w.s.katoms() <= 2 || mx4_rows_little(w.s, rows, PARTS))
-    return launch_token<TX, PARTS, TY, VEC>(X, w, bias, rows, o, Y, w_early, st);
+    return launch_token<TX, PARTS, TY, VEC>(X, Mx4View{}, w, bias, rows, o, Y, w_early, st);
   if constexpr (PARTS > 1) {
     if (rows <= 8) return launch_batch<TX, PARTS, TY, VEC, 1>(X, w, bias, rows, o, Y, w_early, st);
   }
@@ -460,6 +503,18 @@ cudaError_t mx4_rows_fwd(const void* X, int x_dtype, const Mx4View& w, const voi
                                    : launch_rows<__nv_bfloat16, 1, float>(X, w, bias, rows, o, Y, w_early, st);
   return y_dtype == MONARCH_BF16 ? launch_rows<float, 2, __nv_bfloat16>(X, w, bias, rows, o, Y, w_early, st)
                                  : launch_rows<float, 3, float>(X, w, bias, rows, o, Y, w_early, st);
+}
+
+// The tensor-core kernel takes 2.5 us and 0.37 for every 256 inputs, this one 1.7 and 0.6 for 1000 units of work.  us,
+// this one and that: 1 row of 4096 -> 4096 6.0 and 8.6, 16 rows 10.9 and 8.7; 32 of 1024 -> 1024 2.8 and 4.0, 64 5.0 and
+// 4.1; 16 of four 256 -> 1024 blocks 2.4 and 2.9, 32 3.1 and 2.9.
+bool mx4_rows_quantised(const Mx4Shape& w, int64_t rows) {
+  return mx4_rows_work(w, rows) <= 1000 + 550 * ((w.cols + 255) / 256);
+}
+cudaError_t mx4_rows_fwd(const Mx4View& x, const Mx4View& w, const void* bias, const Mx4Out& o, void* Y, int y_dtype, cudaStream_t st) {
+  return y_dtype == MONARCH_BF16
+             ? launch_token<QuantisedX, 1, __nv_bfloat16, true>(nullptr, x, w, bias, x.s.rows, o, Y, false, st)
+             : launch_token<QuantisedX, 1, float, true>(nullptr, x, w, bias, x.s.rows, o, Y, false, st);
 }
 
 }  // namespace monarch

@@ -345,7 +345,8 @@ MONARCH_API int monarch_lattice_bwd(const void* dY, const void* X, const void* c
  *   code = v / 2^e rounded to the nearest of 0, .5, 1, 1.5, 2, 3, 4, 6 (ties to the even code),
  *          cut at 6, with v's sign.
  * A block of zeros has scale byte 0; a block that holds an infinity or a NaN has byte 255 and
- * stands for 32 NaNs.  Values of a row's last block behind `cols` are zeros.
+ * stands for 32 NaNs.  Values of a row's last block behind `cols` are zeros.  Bytes 253 and 254, which
+ * no bf16 or fp32 tensor gives, scale codes of 4 and more out of both types' range: to infinities.
  *
  * A quantised tensor is two caller-owned buffers, 16-byte aligned:
  *   codes   [nblocks][rows][ceil(cols / 32) * 16] bytes, element 2i in the low half of byte i

@@ -204,6 +204,20 @@ def test_linear_forward_of_a_prompt(rows, nb, inn, out, bias, dtype):
     (32, 3, 33, 128, True), (17, 2, 1030, 16, False), (25, 7, 513, 100, True), (8, 1, 4096, 3, True)])
 def test_linear_forward_of_few_tokens(rows, nb, inn, out, bias, dtype):
     test_linear_forward_weights_only(rows, nb, inn, out, bias, dtype)
+    test_linear_forward_both_quantised(rows, nb, inn, out, bias, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [1, 3, 9, 40])
+def test_few_quantised_tokens_agree_with_many(rows, dtype):
+    """The first rows of a long batch and those rows alone: other kernels, sums of the same exact products."""
+    t, v = layer(600, 2, 1056, 200, True, dtype, seed=6)
+    Wq = bdl.mx4_quantise(t["W"])
+    long = bdl.mx4_linear_fwd(bdl.mx4_quantise(t["X"], nblocks=2), Wq, bias=t["b"])
+    alone = bdl.mx4_linear_fwd(bdl.mx4_quantise(t["X"][:rows], nblocks=2), Wq, bias=t["b"])
+    short = {k: (x[:rows] if k in ("x", "xr", "dy") else x) for k, x in v.items()}
+    check_forward(alone, short["xr"], short, 1056, dtype, "Y of a few rows")
+    check_forward(long[:rows], short["xr"], short, 1056, dtype, "first rows of a long batch")
 
 
 # dbias beside dX's product: aligned rows, odd ones, fp32 parts; in a stream of calls that share a workspace, and replayed
