@@ -95,10 +95,10 @@ int check_monarch(const monarch_dims* d) {
 }
 
 // Whether the Monarch map is two products by the few-rows kernels, with the middle vector in fp32 in the workspace;
-// else the factors are expanded there and the plain forward runs.  us, both ways: 200 rows of n = 4096 18.8 and 23.0,
-// 400 33 and 25; 400 of n = 1024 10.1 and 16.5, 1000 20.7 and 17.0; four 256 -> 256 -> 1024 blocks, 100 rows 16 and 33,
-// 400 50 and 36.  The plain forward's generic kernels are slower at any number (1000 rows of four 256 -> 256 -> 256
-// blocks 44 and 461).
+// else the factors are expanded there and the plain forward runs.  us, both ways: 200 rows of n = 4096 20.7 and 23.3,
+// 400 36 and 25; 400 of n = 1024 11.1 and 17.0, 1000 23.0 and 17.6; four 256 -> 256 -> 1024 blocks, 100 rows 17 and 34,
+// 400 56 and 36.  The plain forward's generic kernels are slower at any number (1000 rows of four 256 -> 256 -> 256
+// blocks 47 and 460).
 bool few_rows(const monarch_dims& d) {
   if (d.rows <= 64) return true;
   if (d.rows > kRowsMost) return false;

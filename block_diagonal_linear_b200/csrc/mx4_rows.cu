@@ -3,8 +3,8 @@
 // A decoding step reads the whole weight for a handful of tokens, so the kernels are bound by the
 // latency and bandwidth of that one read (17/32 bytes a weight).  The product runs on mma.sync
 // m16n8k16 with the weights as the 16-row operand and 8 tokens as the columns: codes become bf16
-// values in registers (exact), X enters as one bf16 part, or, in fp32, as 2 or 3 parts that are cut
-// off one after another (3 parts hold all 24 bits; 2 leave 2^-16, below a bf16 result's half step); an MX4 X
+// values in registers (exact), X enters as one bf16 part, or, in fp32 (a Monarch map's middle vector too,
+// whatever the result's type), as 3 parts that are cut off one after another and hold all 24 bits; an MX4 X
 // becomes bf16 values as the weight does.
 //
 // A warp takes 16 outputs and walks scale tiles of 128 inputs: a lane holds one whole scale block of
@@ -16,7 +16,7 @@
 // Up to 8 bf16 tokens, and more where inputs are short or the weight small (mx4_token_kernel), the shares are warps
 // of a CTA and a lane reads its inputs where they are.  Warps that are left take further tiles, or neighbouring blocks: of
 // a transposed result (a Monarch stage) these lie next to each other (32 tokens through sixty-four 64 x 64 blocks
-// twice: 5.5 us, 13.5 with a block a CTA).  With a large weight every warp would gather and cut its own inputs
+// twice: 6.0 us, 14 with a block a CTA).  With a large weight every warp would gather and cut its own inputs
 // too often (4096 -> 4096: 16.5 us for 32 bf16 tokens against 12.2, 12.2 for one in fp32 against 8.1); there
 // (mx4_batch_kernel, up to 64 tokens a pass) the shares are CTAs of a cluster, and a CTA's 8 warps take 128 outputs
 // and share one copy of the inputs in shared memory, already cut into parts, in the order in which lanes read it.
@@ -163,9 +163,9 @@ __device__ __forceinline__ void values(uint4 q, uint32_t e, uint32_t (&a)[16]) {
   }
 }
 // acc += the 32 inputs' products of word v.  mma.sync cuts its sums off (2^-23 a step, always towards
-// zero): an fp32 result takes them in runs of 32 inputs and joins the runs with rounded additions (4096 inputs:
-// 1.3e-6 off without, 1e-7 with).
-template <int PARTS, bool RUNS = PARTS == 3>
+// zero): RUNS, for fp32 operands and fp32 results, takes them in runs of 32 inputs and joins the runs with rounded
+// additions (4096 inputs: 1.3e-6 off without, 1e-7 with).
+template <int PARTS, bool RUNS>
 __device__ __forceinline__ void product(float (&acc)[4], const uint32_t (&a0)[16], const uint32_t (&a1)[16], int v,
                                         const uint32_t (&bp)[PARTS][4]) {
   float run[4] = {};
@@ -192,7 +192,7 @@ template <typename TX, int PARTS, typename TY, bool VEC, int AHEAD>
 __global__ void __launch_bounds__(kWarps * 32, 2)
     mx4_token_kernel(const TX* X, Mx4View xq, Mx4View w, int64_t rows, Mx4Out o, const TY* bias, TY* Y, int lk, int lb, int per,
                      bool w_early) {
-  constexpr bool QX = std::is_same<TX, QuantisedX>::value;
+  constexpr bool QX = std::is_same<TX, QuantisedX>::value, RUNS = PARTS == 3 || sizeof(TY) == 4;
   __shared__ float part[kWarps * kPlane];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   const int wk = 1 << lk, nbw = 1 << lb;
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           const uint32_t bp[1][4] = {{x[4 * v], x[4 * v + 1], x[4 * v + 2], x[4 * v + 3]}};
-          product<1, sizeof(TY) == 4>(acc, a0, a1, v, bp);
+          product<1, RUNS>(acc, a0, a1, v, bp);
         }
       } else {
         uint32_t x[4][8];
@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
         for (int v = 0; v < 4; ++v) {
           uint32_t bp[PARTS][4];
           split8<PARTS>(x[v], bp, (const TX*)nullptr);
-          product<PARTS>(acc, a0, a1, v, bp);
+          product<PARTS, RUNS>(acc, a0, a1, v, bp);
         }
       }
     }
@@ -290,6 +290,7 @@ constexpr int kSumPitch = 20;  // 16 outputs of a token, padded: 16-byte reads, 
 template <typename TX, int PARTS, typename TY, bool VEC, int NT>
 __global__ void __launch_bounds__(kWarps * 32, 2)
     mx4_batch_kernel(const TX* X, Mx4View w, int64_t rows, Mx4Out o, const TY* bias, TY* Y, int shares, int per, bool w_early) {
+  constexpr bool RUNS = PARTS == 3 || sizeof(TY) == 4;
   constexpr int U = sizeof(TX) == 2 ? 8 : 4;  // chunks of 8 inputs a thread asks for before it stores the first
   extern __shared__ uint4 xs[];  // [PARTS][8 * NT][kAhead * 16]
   constexpr int PLANE = 8 * NT * kAhead * 16;
@@ -364,7 +365,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
             const uint4 u = xs[q * PLANE + chunk_at(nt * 8 + g, i * 16 + t * 4 + v)];
             bp[q][0] = u.x; bp[q][1] = u.y; bp[q][2] = u.z; bp[q][3] = u.w;
           }
-          product<PARTS>(acc[nt], a0, a1, v, bp);
+          product<PARTS, RUNS>(acc[nt], a0, a1, v, bp);
         }
       }
     }
@@ -493,7 +494,7 @@ double mx4_rows_work(const Mx4Shape& w, int64_t rows) {
   return (double)w.nblocks * (double)((w.rows + 15) / 16) * w.katoms() * (double)((rows + 7) / 8);
 }
 bool mx4_rows_little(const Mx4Shape& w, int64_t rows, int parts) {
-  return mx4_rows_work(w, rows) <= (parts == 1 ? 5120 : parts == 2 ? 4096 : 3072);
+  return mx4_rows_work(w, rows) <= (parts == 1 ? 5120 : 3072);
 }
 
 cudaError_t mx4_rows_fwd(const void* X, int x_dtype, const Mx4View& w, const void* bias, int64_t rows, const Mx4Out& o, void* Y,
@@ -501,7 +502,7 @@ cudaError_t mx4_rows_fwd(const void* X, int x_dtype, const Mx4View& w, const voi
   if (x_dtype == MONARCH_BF16)
     return y_dtype == MONARCH_BF16 ? launch_rows<__nv_bfloat16, 1, __nv_bfloat16>(X, w, bias, rows, o, Y, w_early, st)
                                    : launch_rows<__nv_bfloat16, 1, float>(X, w, bias, rows, o, Y, w_early, st);
-  return y_dtype == MONARCH_BF16 ? launch_rows<float, 2, __nv_bfloat16>(X, w, bias, rows, o, Y, w_early, st)
+  return y_dtype == MONARCH_BF16 ? launch_rows<float, 3, __nv_bfloat16>(X, w, bias, rows, o, Y, w_early, st)
                                  : launch_rows<float, 3, float>(X, w, bias, rows, o, Y, w_early, st);
 }
 

@@ -360,6 +360,42 @@ def test_monarch_few_tokens_keep_the_middle_vector():
         close(Y, oracle.forward(shape, x, r, l), mags, 70, "bf16", "Y", extra=2.0 ** -16 * mags)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,inn,mid,out", [(1, 4, 2, 3), (8, 40, 64, 130), (20, 33, 250, 70), (64, 64, 1024, 2048), (24, 64, 1024, 2048)])
+def test_monarch_few_tokens_keep_every_bit_of_the_middle_vector(rows, inn, mid, out, dtype):
+    """Middle values of 24 one bits, and beside each the negative of its first 16: the result is the last
+    eight, and every sum on the way to it is exact in fp32."""
+    ones = 255 * np.exp2([-7.0, -15.0, -23.0])
+    X, R, L = np.zeros((rows, inn)), np.zeros((1, mid, inn)), np.zeros((1, out, mid))
+    X[:, :3] = ones * np.exp2(np.arange(rows) % 5)[:, None]
+    R[0, 0::2, :3], R[0, 1::2, :2] = 1, -1
+    for o in range(out):
+        at = 2 * (o % (mid // 2))
+        L[0, o, at:at + 2] = 1
+    shape = dict(nb1=1, in1=inn, out1=mid, nb2=1, in2=mid, out2=out, out_transpose=0)
+    t = [dev(a, dtype)[0] for a in (X, R, L)]
+    Y = bdl.mx4_fwd(t[0], bdl.mx4_quantise(t[1]), bdl.mx4_quantise(t[2]), shape)
+    assert np.array_equal(f64(Y), np.repeat(X[:, 2:3], out, axis=1))
+
+
+@pytest.mark.parametrize("rows", [1, 4, 17, 64])
+def test_monarch_few_tokens_are_rounded_once(rows):
+    """Both sums are fp32 sums of the middle vector's full values: no more than their own rounding on top of half
+    a step of the bf16 result."""
+    for shape in (dict(nb1=32, in1=32, out1=32, nb2=32, in2=32, out2=32, out_transpose=1),
+                  dict(nb1=4, in1=256, out1=256, nb2=4, in2=256, out2=1024, out_transpose=0)):
+        rng = np.random.default_rng(rows)
+        X, x = dev(rng.standard_normal((rows, 1024)), "bf16")
+        R, r = dev(rng.uniform(-1, 1, (shape["nb1"], shape["out1"], shape["in1"])), "bf16")
+        L, l = dev(rng.uniform(-1, 1, (shape["nb2"], shape["out2"], shape["in2"])), "bf16")
+        Y = bdl.mx4_fwd(X, bdl.mx4_quantise(R), bdl.mx4_quantise(L), shape)
+        r, l = oracle.mx4_round(r), oracle.mx4_round(l)
+        mags = oracle.forward(shape, np.abs(x), np.abs(r), np.abs(l))
+        # runs of 32 inputs (two steps that cut off, at most 2^-23 each), then one rounded addition a run
+        terms = sum(2 * 3 + n / 32 for n in (shape["in1"], shape["in2"])) + 2
+        close(Y, oracle.forward(shape, x, r, l), mags, terms, "bf16", "Y")
+
+
 # ---------------------------------------------------------------- as they are used
 def test_training_steps_of_a_quantised_layer():
     """Forward, backward and update of fp32 master weights for three steps: every step's outputs are the
