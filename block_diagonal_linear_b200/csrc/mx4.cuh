@@ -102,6 +102,12 @@ __device__ __forceinline__ void values8(uint32_t w, uint32_t byte, uint32_t (&v)
   v[3] = __byte_perm(p[2], p[3], 0x7632);
 }
 
+// fp32 bits whose upper half is a NaN if they are one: a NaN's payload may lie in the lower half alone, and
+// the upper half by itself would then be an infinity.
+__device__ __forceinline__ uint32_t nan_in_top(uint32_t bits) {
+  return (bits << 1) > 0xff000000u ? bits | 0x00400000u : bits;
+}
+
 // Words o .. o + 4 of eight (o in 0 .. 3).
 __device__ __forceinline__ void pick5(const uint32_t (&w)[8], int o, uint32_t (&r)[5]) {
   uint32_t t[6];

@@ -428,6 +428,8 @@ __device__ __forceinline__ void stage_rows(const StageJob& j, int64_t blk) {
       *dst = make_uint4(x[u][0], x[u][1], x[u][2], x[u][3]);
     } else {
 #pragma unroll
+      for (int i = 0; i < 8; ++i) x[u][i] = mx4::nan_in_top(x[u][i]);
+#pragma unroll
       for (int p = PARTS - 1; p >= 0; --p) {
         uint32_t w[4];
 #pragma unroll

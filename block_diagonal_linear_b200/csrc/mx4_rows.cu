@@ -75,7 +75,7 @@ template <int PARTS>
 __device__ __forceinline__ void split8(const uint32_t (&x)[8], uint32_t (&b)[PARTS][4], const float*) {
   float rest[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) rest[i] = __uint_as_float(x[i]);
+  for (int i = 0; i < 8; ++i) rest[i] = __uint_as_float(mx4::nan_in_top(x[i]));
 #pragma unroll
   for (int p = 0; p < PARTS; ++p) {
 #pragma unroll

@@ -294,6 +294,28 @@ def test_nan_and_infinity_stay_in_their_rows(rows, nb, inn, out):
     assert np.array_equal(np.isnan(f64(dW)), bad_w)
 
 
+@pytest.mark.parametrize("bits", [0x7f800001, -0x7fffff, 0x7f80ffff, 0x7fc00000])
+@pytest.mark.parametrize("rows,nb,inn,out", [(3, 1, 70, 40), (24, 1, 4096, 2048), (200, 2, 256, 300)])
+def test_nan_payloads_in_the_low_half_stay_nan(rows, nb, inn, out, bits):
+    """fp32 operands are cut into bf16 parts: a NaN with nothing in its upper 16 bits but the exponent is one still."""
+    rng = np.random.default_rng(4)
+    X, dY = (dev(rng.standard_normal((rows, nb * n)), "f32")[0] for n in (inn, out))
+    Wq = bdl.mx4_quantise(dev(rng.uniform(0.5, 1, (nb, out, inn)), "f32")[0])   # no zeros: infinities would stay
+    Xq = bdl.mx4_quantise(dev(rng.uniform(0.5, 1, (rows, nb * inn)), "f32")[0], nblocks=nb)
+    X.view(torch.int32)[1, 7] = bits
+    dY.view(torch.int32)[2, 5] = bits
+    Y = f64(bdl.mx4_linear_fwd(X, Wq)).reshape(rows, nb, out)
+    bad = np.zeros(Y.shape, dtype=bool)
+    bad[1, 0] = True
+    assert np.array_equal(np.isnan(Y), bad) and np.isfinite(Y[~bad]).all()
+    dX, dW, db = (f64(g) for g in bdl.mx4_linear_bwd(dY, Xq, Wq, bias=True))
+    bad_x, bad_w, bad_b = np.zeros((rows, nb, inn), dtype=bool), np.zeros(dW.shape, dtype=bool), np.zeros(db.shape, dtype=bool)
+    bad_x[2, 0], bad_w[0, 5], bad_b[5] = True, True, True
+    for g, bad in ((dX.reshape(bad_x.shape), bad_x), (dW, bad_w), (db, bad_b)):
+        assert np.array_equal(np.isnan(g), bad) and np.isfinite(g[~bad]).all()
+    assert np.isnan(f64(bdl.mx4_dequantise(bdl.mx4_quantise(X, nblocks=nb)))[1, :min(32, inn)]).all()
+
+
 def test_extreme_scales():
     """Weights of 2^100 and 2^-100 against activations that bring the products back into range."""
     rng = np.random.default_rng(9)
