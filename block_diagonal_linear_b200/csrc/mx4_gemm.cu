@@ -17,6 +17,10 @@
 // index (rows of 128 swizzled bytes) or its M / N index (chunks of 64 x 64); all tensor maps are per
 // block, so tiles that hang over a block's edge read zeros and write nothing there.  A long K with few
 // tiles is split; the parts are written in fp32 and summed in order.
+// The tensor cores cut their sums off towards zero, which over a long K moves them all the same way (8192 inputs of
+// one sign, fp32: 5.4e-6 too small).  So sums leave TMEM in runs, of 512 inputs for fp32 and of 4096 for bf16 operands; the
+// epilogue, idle under the MMAs of the next run, adds these up in registers with rounded additions (fp32 7e-8 off at any K).  fp32
+// products take 2 to 6 % longer for it (8192 x 4096 -> 4096 549 and 567 us, odd widths up to 10 %), bf16 ones the same time.
 // Roles: warp 0 TMA producer, warp 1 MMA issuer (of the pair's first CTA), warps 2..9 epilogue (two warps a
 // TMEM lane quadrant, alternate 128-byte chunks of columns, each staging and storing its own 32 rows).
 #include <algorithm>
@@ -40,6 +44,7 @@ struct GJob {
   int64_t d_b, d_m, d_s;  // D strides (elements) of a block, a row and a split, for the epilogue without TMA
   int nk, parts;       // K stages of one part; parts of A
   int stages_per_split;
+  int run;             // K stages that TMEM sums before the epilogue takes them over
   int beside;          // run beside the kernel that was launched just before (see the kernel)
   int a_chunks, b_chunks;  // inner index M / N: copies a stage takes (see load_operand)
   int a_bytes, b_bytes;    // of a CTA's stage
@@ -211,39 +216,41 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t dA = C::A_MN ? make_sdesc_lbo(ra, 8192, 1024, 2) : make_sdesc(ra, 1024, 2);
       const uint64_t dB = C::B_MN ? make_sdesc_lbo(rb, 8192, 1024, 2) : make_sdesc(rb, 1024, 2);
       constexpr uint64_t ka = (C::A_MN ? 2048 : 32) >> 4, kb_ = (C::B_MN ? 2048 : 32) >> 4;
-      uint32_t it = 0, n = 0;
+      uint32_t it = 0, n = 0;  // stages and runs
       bool ok = true;
-      for (int64_t u = cl; u < job.units && ok; u += ncl, ++n) {
+      for (int64_t u = cl; u < job.units && ok; u += ncl) {
         const GUnit c = unit_at(job, u);
         int lo, hi;
         stage_range(job, c.split, &lo, &hi);
-        const int slot = n & 1;
-        if (!all_wait_or_abort(&bars->acc_empty[slot], ((n >> 1) & 1) ^ 1, abort_flag, status)) { ok = false; break; }
-        ptx::tc_fence_after();
-        const uint32_t d = tmem + slot * C::BN;
-        for (int kb = lo; kb < hi; ++kb, ++it) {
-          const int st = it % C::NSTAGE;
-          if (!all_wait_or_abort(&bars->full[st], (it / C::NSTAGE) & 1, abort_flag, status)) { ok = false; break; }
+        for (int r0 = lo; r0 < hi && ok; r0 += job.run, ++n) {
+          const int slot = n & 1, r1 = min(hi, r0 + job.run);
+          if (!all_wait_or_abort(&bars->acc_empty[slot], ((n >> 1) & 1) ^ 1, abort_flag, status)) { ok = false; break; }
           ptx::tc_fence_after();
-          const uint64_t soff = (uint64_t)((st * C::STAGE) >> 4);
+          const uint32_t d = tmem + slot * C::BN;
+          for (int kb = r0; kb < r1; ++kb, ++it) {
+            const int st = it % C::NSTAGE;
+            if (!all_wait_or_abort(&bars->full[st], (it / C::NSTAGE) & 1, abort_flag, status)) { ok = false; break; }
+            ptx::tc_fence_after();
+            const uint64_t soff = (uint64_t)((st * C::STAGE) >> 4);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint32_t acc = (kb > lo || kk > 0) ? 1u : 0u;
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint32_t acc = (kb > r0 || kk > 0) ? 1u : 0u;
+              if (PAIR)
+                ptx::mma_bf16_ss_pair_elect(d, dA + soff + kk * ka, dB + soff + kk * kb_, idesc, acc);
+              else
+                ptx::mma_bf16_ss_elect(d, dA + soff + kk * ka, dB + soff + kk * kb_, idesc, acc);
+            }
             if (PAIR)
-              ptx::mma_bf16_ss_pair_elect(d, dA + soff + kk * ka, dB + soff + kk * kb_, idesc, acc);
+              ptx::mma_commit_pair_elect(&bars->empty[st], 0x3);
             else
-              ptx::mma_bf16_ss_elect(d, dA + soff + kk * ka, dB + soff + kk * kb_, idesc, acc);
+              ptx::mma_commit_elect(&bars->empty[st]);
           }
+          if (!ok) break;
           if (PAIR)
-            ptx::mma_commit_pair_elect(&bars->empty[st], 0x3);
+            ptx::mma_commit_pair_elect(&bars->acc_full[slot], 0x3);
           else
-            ptx::mma_commit_elect(&bars->empty[st]);
+            ptx::mma_commit_elect(&bars->acc_full[slot]);
         }
-        if (!ok) break;
-        if (PAIR)
-          ptx::mma_commit_pair_elect(&bars->acc_full[slot], 0x3);
-        else
-          ptx::mma_commit_elect(&bars->acc_full[slot]);
       }
       if (PAIR)
         ptx::mma_commit_pair_elect(&bars->mma_done, 0x3);
@@ -272,10 +279,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     if (bias != nullptr) fetch_bias(cl);
-    uint32_t n = 0;
-    for (int64_t u = cl; u < job.units; u += ncl, ++n) {
+    uint32_t n = 0;  // runs
+    bool ok = true;
+    auto release = [&](int slot) {
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (first)
+          ptx::mbar_arrive(&bars->acc_empty[slot]);
+        else
+          ptx::mbar_arrive_cluster(acc_empty0 + (uint32_t)(slot * sizeof(uint64_t)));
+      }
+    };
+    for (int64_t u = cl; u < job.units; u += ncl) {
       const GUnit c = unit_at(job, u);
-      const int slot = n & 1;
       const int n0 = c.nt * C::BN;
       const int64_t m0 = (int64_t)c.mt * C::BM + (int64_t)rank * 128 + quad * 32;  // this warp's rows
       if (bias != nullptr) {
@@ -285,9 +302,47 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         fetch_bias(u + ncl);  // asked for a tile ahead
       }
-      if (!all_wait_or_abort(&bars->acc_full[slot], (n >> 1) & 1, abort_flag, status)) break;
-      ptx::tc_fence_after();
-      const uint32_t tb = tmem + lane_off + slot * C::BN;
+      int lo, hi;
+      stage_range(job, c.split, &lo, &hi);
+      if (hi - lo > job.run) {
+        // the runs' sums in registers; with the last one they go back to its columns, so that they need not stay
+        // in registers beside the stores
+        constexpr int KEPT = MINE * CC;
+        float kept[KEPT];
+#pragma unroll
+        for (int e = 0; e < KEPT; ++e) kept[e] = 0.f;
+        for (;; lo += job.run, ++n) {
+          if (!(ok = all_wait_or_abort(&bars->acc_full[n & 1], (n >> 1) & 1, abort_flag, status))) break;
+          ptx::tc_fence_after();
+          const bool last = hi - lo <= job.run;
+          const uint32_t at = tmem + lane_off + (n & 1) * C::BN + half * CC;
+#pragma unroll
+          for (int e = 0; e < KEPT; e += 16) {
+            uint32_t t16[16];
+            ptx::tmem_ld16(at + 2 * (e / CC) * CC + e % CC, t16);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) kept[e + k] += __uint_as_float(t16[k]);
+          }
+          if (last) {
+#pragma unroll
+            for (int e = 0; e < KEPT; e += 16) {
+              uint32_t t16[16];
+#pragma unroll
+              for (int k = 0; k < 16; ++k) t16[k] = __float_as_uint(kept[e + k]);
+              ptx::tmem_st16(at + 2 * (e / CC) * CC + e % CC, t16);
+            }
+            ptx::tmem_wait_st();
+            break;
+          }
+          release(n & 1);
+        }
+      } else {
+        ok = all_wait_or_abort(&bars->acc_full[n & 1], (n >> 1) & 1, abort_flag, status);
+        ptx::tc_fence_after();
+      }
+      if (!ok) break;
+      const uint32_t tb = tmem + lane_off + (n & 1) * C::BN;
 #pragma unroll 1
       for (int i = 0; i < MINE; ++i) {
         const int ch = 2 * i + half;
@@ -327,14 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  (int)min((int64_t)32, job.m - m0), job.n - n0 - ch * CC);
         }
       }
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (first)
-          ptx::mbar_arrive(&bars->acc_empty[slot]);
-        else
-          ptx::mbar_arrive_cluster(acc_empty0 + (uint32_t)(slot * sizeof(uint64_t)));
-      }
+      release(n++ & 1);
     }
     if (C::TMA_OUT && lane == 0) ptx::bulk_wait_all();
   }
@@ -729,6 +777,7 @@ cudaError_t gemm(const Operand& a, const Operand& b, const Result& d, const void
   j.nk = (int)((k + 63) / 64);
   j.parts = parts;
   j.stages_per_split = p.per_split;
+  j.run = parts == 1 ? 64 : p.nsplit == 1 && j.nk <= 8 ? 24 : 8;  // 24: one run, in which 8 stages are the leading part's
   const bool tma = d.d_m * sizeof(T) % 16 == 0 && d.d_b * sizeof(T) % 16 == 0 && d.d_s * sizeof(T) % 16 == 0;
   if (p.pair)
     return tma ? launch<GCfg<true, A_MN, B_MN, T, true>>(a, b, d, bias, j, status, st)

@@ -294,6 +294,53 @@ def test_nan_and_infinity_stay_in_their_rows(rows, nb, inn, out):
     assert np.array_equal(np.isnan(f64(dW)), bad_w)
 
 
+def drift(got, ref):
+    """(normwise, signed) error of an fp32 tensor against a float64 one, both on the GPU."""
+    d = got.double() - ref
+    return float(d.norm() / ref.norm()), float((d * ref.sign()).sum() / ref.abs().sum())
+
+
+# Sums of one sign, where cut-off additions all err the same way.  A run of 512 inputs is 32 additions of the leading
+# part that may each cut off 2^-23 of the partial sum, which grows evenly: 16.5 * 2^-23 of the run.  The runs join with
+# additions that are off by at most 2^-24 of a sum that grows as evenly.
+def run_bound(k):
+    return 16.5 * 2.0 ** -23 + (k / 512 / 2 + 1) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("rows,inn,out", [(8192, 8192, 512), (600, 8192, 8192), (300, 16384, 257), (16384, 1000, 300), (8192, 512, 2049)])
+def test_fp32_sums_do_not_drift_with_their_length(rows, inn, out):
+    g = torch.Generator(device="cuda").manual_seed(rows + inn)
+    X, W, dY = (torch.rand(s, generator=g, device="cuda") + 0.01 for s in ((rows, inn), (1, out, inn), (rows, out)))
+    Xq, Wq = bdl.mx4_quantise(X), bdl.mx4_quantise(W)
+    x, w = bdl.mx4_dequantise(Xq).double(), bdl.mx4_dequantise(Wq)[0].double()
+    dX, dW, db = bdl.mx4_linear_bwd(dY, Xq, Wq, bias=True)
+    dy = dY.double()
+    for got, ref, k, what in ((bdl.mx4_linear_fwd(X, Wq), X.double() @ w.T, inn, "Y"), (dX, dy @ w, out, "dX"), (dW[0], dy.T @ x, rows, "dW"),
+                              (db, dy.sum(0), rows, "dbias"), (bdl.mx4_linear_fwd(X[:20].contiguous(), Wq), X[:20].double() @ w.T, inn, "Y of 20 rows")):
+        norm, signed = drift(got, ref)
+        assert norm <= run_bound(k) and abs(signed) <= run_bound(k), (what, k, norm, signed, run_bound(k))
+    assert bdl.last_device_status() == 0
+
+
+def test_bf16_sums_of_a_very_long_batch_do_not_drift():
+    """dW over 262144 rows of one sign: the mean error of 64 x 64 results is a mean of roundings, plus what runs of 4096
+    rows cut off (256 additions, as above)."""
+    rows, n = 1 << 18, 4096
+    g = torch.Generator(device="cuda").manual_seed(1)
+    X = torch.rand((rows, n), generator=g, device="cuda", dtype=torch.bfloat16)
+    Xq = bdl.mx4_quantise(X)
+    x = bdl.mx4_dequantise(Xq)[:, :64].double()
+    dY = X * torch.exp2(torch.arange(n, device="cuda") / 64).bfloat16()   # results spread over a bf16 binade
+    dY[:, n // 2:] = X[:, :n // 2]
+    Wq = bdl.mx4_quantise(torch.ones((1, n, n), device="cuda", dtype=torch.bfloat16))
+    _, dW, _ = bdl.mx4_linear_bwd(dY, Xq, Wq, need_dX=False)
+    ref = dY[:, :64].double().T @ x
+    d = (dW[0, :64, :64].double() - ref) / ref
+    assert float(d.abs().max()) <= 2.0 ** -8 + 128.5 * 2.0 ** -23 + 2.0 ** -17
+    # a rounding to bf16 is off by at most 2^-8 / 2 of the value on average 0: five deviations of 4096 such
+    assert abs(float(d.mean())) <= 128.5 * 2.0 ** -23 + 64 / 2 * 2.0 ** -24 + 5 * 2.0 ** -8 / 3 ** 0.5 / 64
+
+
 @pytest.mark.parametrize("bits", [0x7f800001, -0x7fffff, 0x7f80ffff, 0x7fc00000])
 @pytest.mark.parametrize("rows,nb,inn,out", [(3, 1, 70, 40), (24, 1, 4096, 2048), (200, 2, 256, 300)])
 def test_nan_payloads_in_the_low_half_stay_nan(rows, nb, inn, out, bits):
