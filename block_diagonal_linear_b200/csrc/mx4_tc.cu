@@ -38,6 +38,10 @@ constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr uint32_t kSfCol = 472;  // first TMEM column of the scales
 constexpr int kSlab = 32 * 128;  // a warp's 32 rows x 128 bytes of output
+// The tensor cores cut their sums off towards zero.  Steps of 64 exact products are few: fp32 results of 16384 inputs are
+// 2.3e-7 off at most, but those of 65536 inputs of one sign 4.2e-6 and of 262144 4.7e-5 (1.3e-7 so).  So from here on fp32 results join
+// runs of 4096 inputs with rounded additions, in the 128 x 128 tile.
+constexpr int kRunFrom = 16384;
 
 struct Job {
   int nb, mtiles, ntiles;
@@ -51,9 +55,12 @@ struct Job {
 
 // KEEP: a CTA has one tile of W, whose up to four stages stay in shared memory, and every so many row tiles of
 // X; only X's stages come with every tile.
-template <int BN_, bool PAIR_, bool KEEP_ = false>
+// RUNS: sums leave TMEM every RUN stages and join with rounded additions (see below).
+template <int BN_, bool PAIR_, bool KEEP_ = false, bool RUNS_ = false>
 struct Cfg {
-  static constexpr bool PAIR = PAIR_, KEEP = KEEP_;
+  static constexpr bool PAIR = PAIR_, KEEP = KEEP_, RUNS = RUNS_;
+  static constexpr int RUN = 16;  // 4096 values
+  static_assert(!RUNS || (!KEEP && 2 * BN_ <= (int)kSfCol), "accumulators without common columns");
   static_assert(!(PAIR && KEEP), "pairs share W's tiles already");
   static constexpr int BN = BN_, BM = PAIR ? 256 : 128;  // of a unit; a CTA holds 128 rows
   static constexpr int BROWS = PAIR ? BN / 2 : BN;       // rows of W that a CTA loads
@@ -233,63 +240,66 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t wring_s = ptx::smem_u32(wring);
       const uint64_t dA = make_sdesc(ring_s, 1024, 2), dB = make_sdesc(wring_s, 1024, 2);
       const uint64_t dSA = scale_desc(ring_s + C::A_BYTES), dSB = scale_desc(wring_s + C::B_BYTES);
+      const int run = C::RUNS ? C::RUN : nkb;
       uint32_t it = 0, n = 0, sf = 0;
       bool ok = true;
-      for (int64_t u = u0; u < u1 && ok; u += ustep, ++n) {
-        const int slot = n & 1;
-        // the epilogue has begun the tile before this one (and so finished the one before that, whose
-        // columns this tile takes) and has read the columns that the two share
-        if (n > 0 && !all_wait_or_abort(&bars->acc_next, (n - 1) & 1, abort_flag, status)) { ok = false; break; }
-        ptx::tc_fence_after();
-        const uint32_t d = tmem + slot * C::SLOT1;
-        // BN = 64: every second tile takes the upper half of its scale tile's four columns
-        const uint32_t sfb_off = C::BN == 64 ? 2 * (uint32_t)(unit_at<C::KEEP>(job, u).nt & 1) : 0u;
-        for (int kb = 0; kb < nkb; ++kb, ++it) {
-          const int st = it % C::NSTAGE;
-          if (!all_wait_or_abort(&bars->full[st], (it / C::NSTAGE) & 1, abort_flag, status)) { ok = false; break; }
-          const int ws = C::KEEP ? kb : st;
-          if (C::KEEP && n == 0 && !all_wait_or_abort(&bars->wfull[ws], 0, abort_flag, status)) { ok = false; break; }
+      for (int64_t u = u0; u < u1 && ok; u += ustep) {
+        for (int k0 = 0; k0 < nkb && ok; k0 += run, ++n) {
+          const int slot = n & 1;
+          // the epilogue has begun the tile before this one (and so finished the one before that, whose
+          // columns this tile takes) and has read the columns that the two share
+          if (n > 0 && !all_wait_or_abort(&bars->acc_next, (n - 1) & 1, abort_flag, status)) { ok = false; break; }
           ptx::tc_fence_after();
-          const uint64_t soff = (uint64_t)((st * C::STAGE) >> 4), woff = (uint64_t)((ws * C::WPITCH) >> 4);
-          const int steps = job.ksteps - 4 * kb < 4 ? job.ksteps - 4 * kb : 4;
+          const uint32_t d = tmem + slot * C::SLOT1;
+          // BN = 64: every second tile takes the upper half of its scale tile's four columns
+          const uint32_t sfb_off = C::BN == 64 ? 2 * (uint32_t)(unit_at<C::KEEP>(job, u).nt & 1) : 0u;
+          for (int kb = k0; kb < min(nkb, k0 + run); ++kb, ++it) {
+            const int st = it % C::NSTAGE;
+            if (!all_wait_or_abort(&bars->full[st], (it / C::NSTAGE) & 1, abort_flag, status)) { ok = false; break; }
+            const int ws = C::KEEP ? kb : st;
+            if (C::KEEP && n == 0 && !all_wait_or_abort(&bars->wfull[ws], 0, abort_flag, status)) { ok = false; break; }
+            ptx::tc_fence_after();
+            const uint64_t soff = (uint64_t)((st * C::STAGE) >> 4), woff = (uint64_t)((ws * C::WPITCH) >> 4);
+            const int steps = job.ksteps - 4 * kb < 4 ? job.ksteps - 4 * kb : 4;
 #pragma unroll
-          for (int a = 0; a < 2; ++a) {  // 128 values of K: scale tiles, then two MMAs
-            if (2 * a >= steps) break;
-            const uint32_t sfa = tmem + kSfCol + sf * (4 + 4 * C::NT), sfb = sfa + 4;
-            sf = sf == 2 ? 0 : sf + 1;
+            for (int a = 0; a < 2; ++a) {  // 128 values of K: scale tiles, then two MMAs
+              if (2 * a >= steps) break;
+              const uint32_t sfa = tmem + kSfCol + sf * (4 + 4 * C::NT), sfb = sfa + 4;
+              sf = sf == 2 ? 0 : sf + 1;
+              if (PAIR)
+                ptx::tmem_cp_32x128b_pair_elect(sfa, dSA + soff + a * (512 >> 4));
+              else
+                ptx::tmem_cp_32x128b_elect(sfa, dSA + soff + a * (512 >> 4));
+#pragma unroll
+              for (int j = 0; j < C::NT; ++j) {
+                const uint64_t from = dSB + woff + ((j * 1024 + a * 512) >> 4);
+                if (PAIR)
+                  ptx::tmem_cp_32x128b_pair_elect(sfb + j * 4, from);
+                else
+                  ptx::tmem_cp_32x128b_elect(sfb + j * 4, from);
+              }
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const int kk = 2 * a + k;
+                if (kk >= steps) break;
+                const uint32_t acc = (kb > k0 || kk > 0) ? 1u : 0u;
+                if (PAIR)
+                  ptx::mma_mxf4_ss_pair_elect(d, dA + soff + kk * 2, dB + woff + kk * 2, idesc_mxf4(C::BM, C::BN, k), sfa, sfb, acc);
+                else
+                  ptx::mma_mxf4_ss_elect(d, dA + soff + kk * 2, dB + woff + kk * 2, idesc_mxf4(C::BM, C::BN, k), sfa, sfb + sfb_off, acc);
+              }
+            }
             if (PAIR)
-              ptx::tmem_cp_32x128b_pair_elect(sfa, dSA + soff + a * (512 >> 4));
+              ptx::mma_commit_pair_elect(&bars->empty[st], 0x3);
             else
-              ptx::tmem_cp_32x128b_elect(sfa, dSA + soff + a * (512 >> 4));
-#pragma unroll
-            for (int j = 0; j < C::NT; ++j) {
-              const uint64_t from = dSB + woff + ((j * 1024 + a * 512) >> 4);
-              if (PAIR)
-                ptx::tmem_cp_32x128b_pair_elect(sfb + j * 4, from);
-              else
-                ptx::tmem_cp_32x128b_elect(sfb + j * 4, from);
-            }
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int kk = 2 * a + k;
-              if (kk >= steps) break;
-              const uint32_t acc = (kb > 0 || kk > 0) ? 1u : 0u;
-              if (PAIR)
-                ptx::mma_mxf4_ss_pair_elect(d, dA + soff + kk * 2, dB + woff + kk * 2, idesc_mxf4(C::BM, C::BN, k), sfa, sfb, acc);
-              else
-                ptx::mma_mxf4_ss_elect(d, dA + soff + kk * 2, dB + woff + kk * 2, idesc_mxf4(C::BM, C::BN, k), sfa, sfb + sfb_off, acc);
-            }
+              ptx::mma_commit_elect(&bars->empty[st]);
           }
+          if (!ok) break;
           if (PAIR)
-            ptx::mma_commit_pair_elect(&bars->empty[st], 0x3);
+            ptx::mma_commit_pair_elect(&bars->acc_full[slot], 0x3);
           else
-            ptx::mma_commit_elect(&bars->empty[st]);
+            ptx::mma_commit_elect(&bars->acc_full[slot]);
         }
-        if (!ok) break;
-        if (PAIR)
-          ptx::mma_commit_pair_elect(&bars->acc_full[slot], 0x3);
-        else
-          ptx::mma_commit_elect(&bars->acc_full[slot]);
       }
       if (PAIR)
         ptx::mma_commit_pair_elect(&bars->mma_done, 0x3);
@@ -321,10 +331,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     if (bias != nullptr) fetch_bias(u0);
+    auto next = [&] {  // the MMAs may begin the next accumulator
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (first)
+          ptx::mbar_arrive(&bars->acc_next);
+        else
+          ptx::mbar_arrive_cluster(next0);
+      }
+    };
     uint32_t n = 0, stored = 0;
     for (int64_t u = u0; u < u1; u += ustep, ++n) {
       const Unit c = unit_at<C::KEEP>(job, u);
-      const int slot = n & 1;
       const int n0 = c.nt * C::BN;
       const int64_t m0 = (int64_t)c.mt * C::BM + (int64_t)rank * 128 + quad * 32;  // this warp's rows
       if (bias != nullptr) {
@@ -334,8 +353,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         fetch_bias(u + ustep);  // asked for a tile ahead: the epilogue has no time to wait for it
       }
-      if (!all_wait_or_abort(&bars->acc_full[slot], (n >> 1) & 1, abort_flag, status)) break;
-      ptx::tc_fence_after();
+      if constexpr (C::RUNS) {
+        constexpr int KEPT = MINE * CC;
+        float kept[KEPT];
+        bool ok = true;
+#pragma unroll
+        for (int e = 0; e < KEPT; ++e) kept[e] = 0.f;
+        for (int left = nkb;; left -= C::RUN, ++n) {
+          if (!(ok = all_wait_or_abort(&bars->acc_full[n & 1], (n >> 1) & 1, abort_flag, status))) break;
+          ptx::tc_fence_after();
+          const uint32_t at = tmem + lane_off + (n & 1) * C::SLOT1 + half * CC;
+#pragma unroll
+          for (int e = 0; e < KEPT; e += 16) {
+            uint32_t t16[16];
+            ptx::tmem_ld16(at + 2 * (e / CC) * CC + e % CC, t16);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              kept[e + k] += __uint_as_float(t16[k]);
+              t16[k] = __float_as_uint(kept[e + k]);
+            }
+            if (left <= C::RUN) ptx::tmem_st16(at + 2 * (e / CC) * CC + e % CC, t16);  // for the stores below
+          }
+          if (left <= C::RUN) break;
+          next();
+        }
+        if (!ok) break;
+        ptx::tmem_wait_st();
+      } else {
+        if (!all_wait_or_abort(&bars->acc_full[n & 1], (n >> 1) & 1, abort_flag, status)) break;
+        ptx::tc_fence_after();
+      }
+      const int slot = n & 1;
       const uint32_t tb = tmem + lane_off + slot * C::SLOT1;
 #pragma unroll 1
       for (int i = 0; i < MINE; ++i) {
@@ -353,16 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           ptx::tmem_wait_ld();
         }
-        if (i == 0) {
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if (first)
-              ptx::mbar_arrive(&bars->acc_next);
-            else
-              ptx::mbar_arrive_cluster(next0);
-          }
-        }
+        if (i == 0) next();
         if (!live) continue;
         if (bias != nullptr) {
           const float* bs = bias_s + (ch >> 1) * CC;
@@ -500,6 +540,11 @@ cudaError_t launch_out(const Mx4View& x, const Mx4View& w, const void* bias, con
 template <typename T>
 cudaError_t launch_type(const Mx4View& x, const Mx4View& w, const void* bias, const Mx4Linear& d, void* Y, int* status,
                         cudaStream_t st) {
+  if constexpr (sizeof(T) == 4) {
+    if (d.in > kRunFrom)
+      return d.out % 4 == 0 ? launch<Cfg<128, false, false, true>, float, true>(x, w, bias, d, Y, status, st)
+                            : launch<Cfg<128, false, false, true>, float, false>(x, w, bias, d, Y, status, st);
+  }
   // The tile whose rounds over the SMs take the least time: a tile costs a stage's share of the way from
   // L2 for every 256 inputs, and its epilogue.  Microseconds from 8192 rows -> 4096 (256 x 256 pairs, 128 x 256
   // single, 128 x 256 with W kept): 19.8, 14.0 and 15.0 with 256 inputs, 22.5, 17.5 and 17.2 with 512, 26.9, 27.4 and

@@ -322,6 +322,24 @@ def test_fp32_sums_do_not_drift_with_their_length(rows, inn, out):
     assert bdl.last_device_status() == 0
 
 
+@pytest.mark.parametrize("rows,inn,out,bias", [(260, 65536, 257, True), (300, 262144, 132, False), (129, 16385, 1001, True)])
+def test_fp32_results_of_two_quantised_operands_do_not_drift(rows, inn, out, bias):
+    """Steps of 64 inputs that may each cut off 2^-23 of a sum that grows evenly, in runs of 4096."""
+    g = torch.Generator(device="cuda").manual_seed(inn)
+    X, W = (torch.rand(s, generator=g, device="cuda") + 0.01 for s in ((rows, inn), (1, out, inn)))
+    # a scale of its own for every 32, so that sums are not whole numbers of a common step
+    X *= torch.exp(torch.randn((rows, -(-inn // 32)), generator=g, device="cuda")).repeat_interleave(32, 1)[:, :inn]
+    W *= torch.exp(torch.randn((1, out, -(-inn // 32)), generator=g, device="cuda")).repeat_interleave(32, 2)[:, :, :inn]
+    b = torch.randn(out, generator=g, device="cuda") if bias else None
+    Xq, Wq = bdl.mx4_quantise(X), bdl.mx4_quantise(W)
+    ref = bdl.mx4_dequantise(Xq).double() @ bdl.mx4_dequantise(Wq)[0].double().T + (b.double() if bias else 0)
+    Y = bdl.mx4_linear_fwd(Xq, Wq, bias=b)
+    bound = 65 / 2 * 2.0 ** -23 + (inn / 4096 / 2 + 1) * 2.0 ** -24
+    norm, signed = drift(Y, ref)
+    assert norm <= bound and abs(signed) <= bound and bdl.last_device_status() == 0, (norm, signed, bound)
+    assert torch.equal(Y, bdl.mx4_linear_fwd(Xq, Wq, bias=b))
+
+
 def test_bf16_sums_of_a_very_long_batch_do_not_drift():
     """dW over 262144 rows of one sign: the mean error of 64 x 64 results is a mean of roundings, plus what runs of 4096
     rows cut off (256 additions, as above)."""
