@@ -101,13 +101,16 @@ int check_monarch(const monarch_dims* d) {
 // blocks 47 and 460).
 bool few_rows(const monarch_dims& d) {
   if (d.rows <= 64) return true;
-  if (d.rows > kRowsMost) return false;
   return mx4_rows_work(r_shape(d), d.rows) + mx4_rows_work(l_shape(d), d.rows) <= 13000 || monarch_fwd_path(&d) == 0;
 }
 
+// The few-rows kernels take a Monarch map this many rows at a time, with room for the middle vectors of so many.
+constexpr int64_t kMonarchPass = 65536;
+static_assert(kMonarchPass <= kRowsMost, "rows of one launch");
+
 size_t monarch_workspace(const monarch_dims& d) {
   const Shape s = to_shape(d);
-  if (few_rows(d)) return al256((size_t)(s.rows * s.n_mid() * 4));
+  if (few_rows(d)) return al256((size_t)(std::min(s.rows, kMonarchPass) * s.n_mid() * 4));
   const int64_t es = elem_bytes(d.dtype);
   return al256((size_t)(s.n_R() * es)) + al256((size_t)(s.n_L() * es));
 }
@@ -263,12 +266,16 @@ int monarch_mx4_fwd(const void* X, const void* r_codes, const void* r_scales, co
   if (few_rows(*d)) {
     // U = blockdiag(R) X, written through P, then blockdiag(L) of contiguous slices, through P_out.  The
     // second kernel may ask for L at once: whatever wrote it had ended when the first began.
-    if (mx4_rows_fwd(X, d->dtype, r, nullptr, s.rows, Mx4Out::transposed(s.nb1, s.out1), workspace, MONARCH_F32, false, st) !=
-        cudaSuccess)
-      return MONARCH_ERR_CUDA;
-    return status_of(mx4_rows_fwd(workspace, MONARCH_F32, l, nullptr, s.rows,
-                                  s.out_transpose ? Mx4Out::transposed(s.nb2, s.out2) : Mx4Out::blocks(s.nb2, s.out2), Y,
-                                  d->dtype, true, st));
+    const Mx4Out out = s.out_transpose ? Mx4Out::transposed(s.nb2, s.out2) : Mx4Out::blocks(s.nb2, s.out2);
+    for (int64_t r0 = 0; r0 < s.rows; r0 += kMonarchPass) {
+      const int64_t rows = std::min(s.rows - r0, kMonarchPass);
+      const char* x = (const char*)X + r0 * s.n_in() * es;
+      char* y = (char*)Y + r0 * s.n_out() * es;
+      if (mx4_rows_fwd(x, d->dtype, r, nullptr, rows, Mx4Out::transposed(s.nb1, s.out1), workspace, MONARCH_F32, false, st) != cudaSuccess ||
+          mx4_rows_fwd(workspace, MONARCH_F32, l, nullptr, rows, out, y, d->dtype, true, st) != cudaSuccess)
+        return MONARCH_ERR_CUDA;
+    }
+    return MONARCH_OK;
   }
   char* R = (char*)workspace;
   char* L = R + al256((size_t)(s.n_R() * es));

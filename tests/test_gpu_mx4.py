@@ -483,6 +483,25 @@ def test_monarch_few_tokens_are_rounded_once(rows):
         close(Y, oracle.forward(shape, x, r, l), mags, terms, "bf16", "Y")
 
 
+@pytest.mark.parametrize("rows,mid", [(524281, 60000), (524289, 24), (65537, 24), (131072, 40)])
+def test_monarch_rows_beyond_one_launch(rows, mid):
+    """The first and last rows of every pass of 65536, as if they had come alone; nothing behind the last."""
+    shape = dict(nb1=1, in1=8, out1=mid, nb2=1, in2=mid, out2=8, out_transpose=0)
+    g = torch.Generator(device="cuda").manual_seed(mid)
+    R, L = (torch.randn(s, generator=g, device="cuda").bfloat16() for s in ((1, mid, 8), (1, 8, mid)))
+    Rq, Lq = bdl.mx4_quantise(R), bdl.mx4_quantise(L)
+    X = torch.randn((rows, 8), generator=g, device="cuda").bfloat16()
+    Y, ok = guarded((rows, 8), torch.bfloat16)
+    bdl.mx4_fwd(X, Rq, Lq, shape, Y=Y)
+    assert ok() and bdl.last_device_status() == 0
+    at = torch.tensor([r for p in range(0, rows, 65536) for r in (p, min(p + 65535, rows - 1))], device="cuda")
+    r, l = oracle.mx4_round(f64(R)), oracle.mx4_round(f64(L))
+    x = f64(X[at])
+    ref, mags = oracle.forward(shape, x, r, l), oracle.forward(shape, np.abs(x), np.abs(r), np.abs(l))
+    close(Y[at], ref, mags, 8 + mid / 32 + 8, "bf16", "Y")
+    assert bool(torch.isfinite(Y).all()) and float((Y.abs().sum(1) == 0).sum()) == 0
+
+
 # ---------------------------------------------------------------- as they are used
 def test_training_steps_of_a_quantised_layer():
     """Forward, backward and update of fp32 master weights for three steps: every step's outputs are the

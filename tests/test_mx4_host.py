@@ -195,6 +195,18 @@ def test_monarch_refusals():
     assert g(bdl.make_dims(shape, 0, "bf16"), X=None, Y=None) == 0
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_monarch_rows_beyond_one_launch_keep_their_kernels(dtype):
+    """Factors that the plain forward has no tensor-core kernel for, here none at all: the few-token kernels take any number
+    of rows, so many at a time, in one and the same workspace."""
+    L = bdl.lib()
+    shape = dict(nb1=1, in1=8, out1=60000, nb2=1, in2=60000, out2=8, out_transpose=0)
+    assert bdl.fwd_path(shape, dtype) == 0
+    need = [L.monarch_mx4_fwd_workspace_bytes(ctypes.byref(bdl.make_dims(shape, r, dtype))) for r in (65536, 65537, 524280, 524281, 1 << 24)]
+    assert need == [65536 * 60000 * 4] * 5
+    assert L.monarch_mx4_fwd_workspace_bytes(ctypes.byref(bdl.make_dims(shape, 100, dtype))) == 100 * 60000 * 4
+
+
 # ---------------------------------------------------------------- binding refusals (CPU tensors)
 def fake(rows, nb, cols, by_block, dtype="bf16"):
     d = bdl.MonarchMx4Dims(rows, nb, cols, int(by_block), bdl.dtype_code(dtype))
