@@ -1,5 +1,7 @@
-"""Build libmonarch.so in-tree with nvcc for sm_100a, and _mx4_native.so, the native half of the MX4
-binding, with g++ against the installed torch.
+"""Build libmonarch.so in-tree with nvcc for sm_100a, and then _mx4_native.so, the native half of the MX4
+binding, with g++ against the installed torch.  The C ABI needs the first alone: where torch, its CUDA
+libraries, Python's headers or a C++ compiler are missing, the second is left out with a warning, and the MX4
+binding says so at its first use.
 
 Usage: python -m block_diagonal_linear_b200.build  (or call build()).
 """
@@ -8,6 +10,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -44,16 +47,27 @@ def _stale(target: str, sources) -> bool:
     return any(os.path.getmtime(p) > t for p in deps)
 
 
-def _build_native(verbose: bool):
+def native_key(torch) -> str:
+    """What _mx4_native.so is built for: it reads torch's C++ objects through this version's headers."""
+    return "mx4 native: torch %s, cxx11 abi %d, %s" % (torch.__version__, torch.compiled_with_cxx11_abi(), sys.implementation.cache_tag)
+
+
+def _native_stale(torch) -> bool:
+    if _stale(NATIVE_LIB, [NATIVE_SOURCE]):
+        return True
+    with open(NATIVE_LIB, "rb") as f:
+        return native_key(torch).encode() + b"\0" not in f.read()
+
+
+def _build_native(torch, verbose: bool):
     import sysconfig
 
-    import torch
     base = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(_nvcc())) or "/usr/local/cuda"
     include = [os.path.join(base, "include"), os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
     tmp = NATIVE_LIB + ".tmp%d" % os.getpid()
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch.compiled_with_cxx11_abi(), *(a for p in include for a in ("-isystem", p)),
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch.compiled_with_cxx11_abi(), '-DMX4_NATIVE_KEY="%s"' % native_key(torch), *(a for p in include for a in ("-isystem", p)),
            NATIVE_SOURCE, "-o", tmp, "-L" + os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
     if verbose:
         print(" ".join(cmd), flush=True)
@@ -62,8 +76,19 @@ def _build_native(verbose: bool):
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if force or _stale(NATIVE_LIB, [NATIVE_SOURCE]):
-        _build_native(verbose)
+    _build_lib(force, verbose)
+    try:
+        import torch
+        if force or _native_stale(torch):
+            _build_native(torch, verbose)
+    except (ImportError, OSError, subprocess.CalledProcessError) as e:
+        if os.path.exists(NATIVE_LIB) and _stale(NATIVE_LIB, [NATIVE_SOURCE]):
+            os.remove(NATIVE_LIB)  # of older sources: it must not be taken for theirs
+        warnings.warn("_mx4_native.so was not built (%s): the MX4 operators are left to the C entry points" % e)
+    return LIB
+
+
+def _build_lib(force: bool, verbose: bool) -> str:
     if not force and not _stale(LIB, [os.path.join(CSRC, f) for f in SOURCES + HEADERS]):
         return LIB
     objs = []

@@ -337,4 +337,11 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_mx4_native", nullptr, -1, methods
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__mx4_native() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__mx4_native() {
+  PyObject* m = PyModule_Create(&module);
+  if (m != nullptr && PyModule_AddStringConstant(m, "key", MX4_NATIVE_KEY) != 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

@@ -18,6 +18,7 @@ import struct
 
 import torch
 
+from .build import native_key
 from . import MONARCH_BF16, MONARCH_F32, MonarchMx4Dims, MonarchMx4LinearDims, _check, dtype_code, lib
 
 _ENTRY_POINTS = ("monarch_mx4_code_bytes", "monarch_mx4_scale_bytes", "monarch_mx4_quantise", "monarch_mx4_dequantise",
@@ -28,10 +29,13 @@ _ENTRY_POINTS = ("monarch_mx4_code_bytes", "monarch_mx4_scale_bytes", "monarch_m
 def _load():
     """The native half (csrc/mx4_native.cpp), given libmonarch's entry points in the order it takes them."""
     L = lib()
+    again = "; run `python -m block_diagonal_linear_b200.build`"
     try:
         from . import _mx4_native
     except ImportError as e:
-        raise RuntimeError("_mx4_native.so is not built for this torch; run `python -m block_diagonal_linear_b200.build --force`") from e
+        raise RuntimeError("_mx4_native.so is not built, or not for this torch" + again) from e
+    if getattr(_mx4_native, "key", None) != native_key(torch):
+        raise RuntimeError("_mx4_native.so is built for %r, this is %r%s" % (getattr(_mx4_native, "key", None), native_key(torch), again))
     _mx4_native.init(tuple(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in _ENTRY_POINTS), _check)
     return _mx4_native
 
