@@ -110,6 +110,14 @@ struct Workspace {
     n = (size_t)hold.nbytes();
   }
 };
+bool truth(PyObject* o, const char* name) {
+  const int r = PyObject_IsTrue(o);
+  if (r < 0) {
+    PyErr_Clear();
+    bad(std::string(name) + " must be true or false");
+  }
+  return r == 1;
+}
 void* ptr(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 
 // f(stream) with `device` the current one, without the interpreter lock; raises on an error code.
@@ -265,6 +273,10 @@ PyObject* linear_mx4(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* linear_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   arguments(n, 9);
+  const bool want_x = truth(a[3], "need_dX"), want_b = truth(a[4], "bias");
+  if (a[1] == Py_None && a[6] != Py_None) bad("dW needs X");
+  if (!want_x && a[5] != Py_None) bad("dX is given, and need_dX is false");
+  if (!want_b && a[7] != Py_None) bad("dbias is given, and bias is false");
   const Quantised& w = quantised(a[2], "W");
   const Quantised* x = a[1] == Py_None ? nullptr : &quantised(a[1], "X");
   if (!THPVariable_Check(a[0])) bad("dY must be a tensor");
@@ -272,12 +284,10 @@ PyObject* linear_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t dtype = dtype_of(dY, "dY"), rows = dY.dim() > 0 ? dY.size(0) : 0, n_in = w.nblocks * w.cols, n_out = w.nblocks * w.rows;
   if (dY.dim() != 2 || dY.size(1) != n_out) bad("dY must have shape " + shape_of({rows, n_out}) + ", its shape is " + shape_of(dY.sizes()));
   if (x != nullptr && x->rows != rows) bad("X has " + std::to_string(x->rows) + " rows, dY " + std::to_string(rows));
-  if (x == nullptr && a[6] != Py_None) bad("dW needs X");
   tensor(a[0], "dY");
   const int64_t device = dY.get_device();
   on_device(w, "W", device);
   if (x != nullptr) on_device(*x, "X", device);
-  const bool want_x = PyObject_IsTrue(a[3]) == 1, want_b = PyObject_IsTrue(a[4]) == 1;
   const at::Tensor dX = want_x ? output(a[5], "dX", {rows, n_in}, dtype, device) : at::Tensor();
   const at::Tensor dW = x != nullptr ? output(a[6], "dW", {w.nblocks, w.rows, w.cols}, dtype, device) : at::Tensor();
   const at::Tensor db = want_b ? output(a[7], "dbias", {n_out}, dtype, device) : at::Tensor();

@@ -173,7 +173,7 @@ def mx4_linear_fwd(X, W: Mx4, bias=None, Y=None, dtype=None, workspace=None, str
     """Block-diagonal linear layer with W in MX4: Y[r, b*out + o] = sum_i X[r, b*in + i] W[b, o, i] + bias.
 
     X is a plain tensor (rows, nblocks * in_blk), or an Mx4 of one; then Y has `dtype` (default: the type
-    X was quantised from)."""
+    X was quantised from), and no workspace is needed: one that is given is left as it is."""
     _weight(W)
     if isinstance(X, Mx4):
         _activations(X, W)
@@ -189,7 +189,7 @@ def mx4_linear_bwd(dY, X, W, bias: bool = False, need_dX: bool = True, dX=None, 
                    stream=None):
     """(dX, dW, dbias) of mx4_linear_fwd(X, W) for its quantised operands; a training step passes them on
     to the tensors X and W were rounded from.  X = None (a frozen layer) leaves out dW; need_dX = False
-    leaves out dX; dbias is None without `bias`."""
+    leaves out dX; dbias is None without `bias`.  A buffer for a gradient that is not asked for is refused."""
     _weight(W)
     if X is not None:
         if not isinstance(X, Mx4):

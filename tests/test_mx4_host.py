@@ -291,6 +291,20 @@ def test_binding_refuses_streams_and_memory_of_other_devices():
             bdl.mx4_dequantise(bad)
 
 
+def test_backward_refuses_buffers_that_it_would_not_fill():
+    W, Xq = fake(96, 2, 64, True), fake(5, 2, 64, False)
+    dY, dX = torch.zeros(5, 192, dtype=torch.bfloat16), torch.zeros(5, 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="need_dX is false"):
+        bdl.mx4_linear_bwd(dY, Xq, W, need_dX=False, dX=dX)
+    with pytest.raises(ValueError, match="bias is false"):
+        bdl.mx4_linear_bwd(dY, Xq, W, dbias=torch.zeros(192, dtype=torch.bfloat16))
+    with pytest.raises(ValueError, match="dW needs X"):
+        bdl.mx4_linear_bwd(dY, None, W, dW=torch.zeros(2, 96, 64, dtype=torch.bfloat16))
+    for name in ("need_dX", "bias"):
+        with pytest.raises(ValueError, match=name + " must be true or false"):
+            bdl.mx4_linear_bwd(dY, Xq, W, **{name: torch.zeros(2)})
+
+
 def test_copies_have_memory_of_their_own():
     import copy
     import pickle
