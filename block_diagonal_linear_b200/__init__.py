@@ -52,7 +52,8 @@ EXPORTED = (
     "monarch_lattice_path", "monarch_lattice_weight_elems", "monarch_lattice_fwd", "monarch_lattice_bwd",
     "monarch_mx4_code_bytes", "monarch_mx4_scale_bytes", "monarch_mx4_quantise", "monarch_mx4_dequantise",
     "monarch_mx4_linear_wfwd_workspace_bytes", "monarch_mx4_linear_bwd_workspace_bytes",
-    "monarch_mx4_linear_fwd", "monarch_mx4_linear_wfwd", "monarch_mx4_linear_bwd", "monarch_mx4_fwd_workspace_bytes", "monarch_mx4_fwd",
+    "monarch_mx4_linear_path", "monarch_mx4_linear_fwd", "monarch_mx4_linear_wfwd", "monarch_mx4_linear_bwd",
+    "monarch_mx4_fwd_workspace_bytes", "monarch_mx4_fwd_path", "monarch_mx4_fwd",
 )
 
 
@@ -214,6 +215,7 @@ def lib() -> ctypes.CDLL:
                 ("monarch_mx4_linear_fwd", [vp, vp, vp, vp, vp, mp, vp, vp], ctypes.c_int),
                 ("monarch_mx4_linear_wfwd", [vp, vp, vp, vp, mp, vp, vp, sz, vp], ctypes.c_int),
                 ("monarch_mx4_linear_bwd", [vp, vp, vp, vp, vp, mp, vp, vp, vp, vp, sz, vp], ctypes.c_int),
+                ("monarch_mx4_linear_path", [mp, ctypes.c_int], ctypes.c_int), ("monarch_mx4_fwd_path", [dp], ctypes.c_int),
                 ("monarch_mx4_fwd_workspace_bytes", [dp], sz),
                 ("monarch_mx4_fwd", [vp, vp, vp, vp, vp, dp, vp, vp, sz, vp], ctypes.c_int)):
             getattr(L, name).argtypes, getattr(L, name).restype = args, res
@@ -711,7 +713,8 @@ def status_string(code: int) -> str:
 
 
 # ---------------------------------------------------------------- microscaled 4-bit (MX4)
-_MX4 = ("Mx4", "mx4_quantise", "mx4_dequantise", "mx4_linear_fwd", "mx4_linear_bwd", "mx4_linear_workspace_bytes", "mx4_fwd")
+_MX4 = ("Mx4", "mx4_quantise", "mx4_dequantise", "mx4_linear_fwd", "mx4_linear_bwd", "mx4_linear_workspace_bytes", "mx4_linear_path",
+        "mx4_fwd", "mx4_fwd_path")
 
 
 def __getattr__(name: str):

@@ -161,6 +161,22 @@ size_t monarch_mx4_linear_bwd_workspace_bytes(const monarch_mx4_linear_dims* d) 
   return check(d) != MONARCH_OK ? 0 : bwd_workspace(to_linear(*d));
 }
 
+int monarch_mx4_linear_path(const monarch_mx4_linear_dims* ld, int product) {
+  if (check(ld) != MONARCH_OK) return -1;
+  const Mx4Linear d = to_linear(*ld);
+  switch (product) {
+    case 0: return mx4_rows_quantised(d.w(), d.rows) ? kMx4Token : mx4_tc_path(d);
+    case 1: return few_rows(d) ? mx4_rows_path(d.w(), d.rows, d.dtype == MONARCH_BF16 ? 1 : 3) : mx4_gemm_fwd_path(d);
+    case 2: return mx4_gemm_dx_path(d);
+    case 3: return mx4_gemm_dw_path(d);
+    default: return -1;
+  }
+}
+int monarch_mx4_fwd_path(const monarch_dims* d) {
+  if (check_monarch(d) != MONARCH_OK) return -1;
+  return few_rows(*d) ? 0 : monarch_fwd_path(d);
+}
+
 int monarch_mx4_linear_fwd(const void* x_codes, const void* x_scales, const void* w_codes, const void* w_scales,
                            const void* bias, const monarch_mx4_linear_dims* ld, void* Y, void* stream) {
   int rc = check(ld);

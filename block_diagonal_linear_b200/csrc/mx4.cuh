@@ -233,9 +233,17 @@ struct Mx4Linear {
   Mx4Shape x() const { return Mx4Shape{rows, nb, in}; }
   Mx4Shape w() const { return Mx4Shape{out, nb, in}; }
 };
+// Kernels of the products, as monarch_mx4_linear_path names them.
+enum Mx4Path {
+  kMx4Token = 0, kMx4Batch = 1,                                                                        // mx4_rows.cu
+  kMx4Tile64 = 2, kMx4Tile128 = 3, kMx4Tile256 = 4, kMx4Kept = 5, kMx4Pair = 6, kMx4Runs = 7,         // mx4_tc.cu
+  kMx4Gemm = 8, kMx4GemmPair = 9, kMx4Split = 16,                                                      // mx4_gemm.cu; + if K is split
+};
+
 // Both operands in MX4 on the block-scaled tensor cores, every size and both types (mx4_tc.cu).
 cudaError_t mx4_tc_fwd(const Mx4View& x, const Mx4View& w, const void* bias, const Mx4Linear& d, void* Y, int* status,
                        cudaStream_t st);
+int mx4_tc_path(const Mx4Linear& d);
 // What the direct few-rows kernel does, in products of 16 outputs, 128 inputs and 8 tokens, and whether that is little
 // (6 us or so) where X comes in `parts` bf16 parts.
 double mx4_rows_work(const Mx4Shape& w, int64_t rows);
@@ -245,11 +253,15 @@ constexpr int64_t kRowsMost = 8 * 65535;  // rows that the few-rows kernels take
 // run writes the weight, so it may be read ahead of the grid-dependency wait.
 cudaError_t mx4_rows_fwd(const void* X, int x_dtype, const Mx4View& w, const void* bias, int64_t rows, const Mx4Out& o, void* Y,
                          int y_dtype, bool w_early, cudaStream_t st);
+int mx4_rows_path(const Mx4Shape& w, int64_t rows, int parts);
 // The same with X in MX4, and whether that is quicker than the tensor-core kernel for both operands in MX4.
 bool mx4_rows_quantised(const Mx4Shape& w, int64_t rows);
 cudaError_t mx4_rows_fwd(const Mx4View& x, const Mx4View& w, const void* bias, const Mx4Out& o, void* Y, int y_dtype, cudaStream_t st);
 // Products with a plain operand on the bf16 tensor cores, every size and both types (mx4_gemm.cu); ws: the
 // bytes that the size query gives.  dX, dW and dbias may be NULL.
+int mx4_gemm_fwd_path(const Mx4Linear& d);
+int mx4_gemm_dx_path(const Mx4Linear& d);
+int mx4_gemm_dw_path(const Mx4Linear& d);
 size_t mx4_gemm_fwd_bytes(const Mx4Linear& d);
 cudaError_t mx4_gemm_fwd(const void* X, const Mx4View& w, const void* bias, const Mx4Linear& d, void* Y, void* ws, int* status,
                          cudaStream_t st);

@@ -883,6 +883,11 @@ BwdWs bwd_layout(const Mx4Linear& d) {
 
 }  // namespace
 
+static int path_of(const Plan& p) { return (p.pair ? kMx4GemmPair : kMx4Gemm) + (p.nsplit > 1 ? kMx4Split : 0); }
+int mx4_gemm_fwd_path(const Mx4Linear& d) { return path_of(fwd_plan(d)); }
+int mx4_gemm_dx_path(const Mx4Linear& d) { return path_of(dx_plan(d)); }
+int mx4_gemm_dw_path(const Mx4Linear& d) { return path_of(dw_plan(d)); }
+
 size_t mx4_gemm_fwd_bytes(const Mx4Linear& d) { return expanded_bytes(d.w()) + staged_bytes(d, d.in) + fwd_part_bytes(d); }
 
 cudaError_t mx4_gemm_fwd(const void* X, const Mx4View& w, const void* bias, const Mx4Linear& d, void* Y, void* ws, int* status,

@@ -468,7 +468,7 @@ cudaError_t launch_vec(const void* X, const Mx4View& w, const void* bias, int64_
   // 8 tokens is little work.  us, direct and batch: 32 bf16 tokens of sixty-four 64 -> 64 blocks 2.2 and 4.1, 64 of
   // 256 -> 4096 4.9 and 6.9, 32 of 1024 -> 1024 2.6 and 5.3, of 1024 -> 4096 7.9 and 7.2, of 4096 -> 4096 16.5 and 12.2; 16
   // fp32 tokens of 1024 -> 1024 3.8 and 5.2, of 1024 -> 4096 10.1 and 6.9
-  if ((PARTS == 1 && rows <= 8) || w.s.katoms() <= 2 || mx4_rows_little(w.s, rows, PARTS))
+  if (mx4_rows_path(w.s, rows, PARTS) == kMx4Token)
     return launch_token<TX, PARTS, TY, VEC>(X, Mx4View{}, w, bias, rows, o, Y, w_early, st);
   if constexpr (PARTS > 1) {
     if (rows <= 8) return launch_batch<TX, PARTS, TY, VEC, 1>(X, w, bias, rows, o, Y, w_early, st);
@@ -495,6 +495,10 @@ double mx4_rows_work(const Mx4Shape& w, int64_t rows) {
 }
 bool mx4_rows_little(const Mx4Shape& w, int64_t rows, int parts) {
   return mx4_rows_work(w, rows) <= (parts == 1 ? 5120 : 3072);
+}
+
+int mx4_rows_path(const Mx4Shape& w, int64_t rows, int parts) {
+  return (parts == 1 && rows <= 8) || w.katoms() <= 2 || mx4_rows_little(w, rows, parts) ? kMx4Token : kMx4Batch;
 }
 
 cudaError_t mx4_rows_fwd(const void* X, int x_dtype, const Mx4View& w, const void* bias, int64_t rows, const Mx4Out& o, void* Y,

@@ -530,21 +530,17 @@ cudaError_t launch(const Mx4View& x, const Mx4View& w, const void* bias, const M
   return e;
 }
 
-template <int BN, bool PAIR, typename T>
+template <class C, typename T>
 cudaError_t launch_out(const Mx4View& x, const Mx4View& w, const void* bias, const Mx4Linear& d, void* Y, int* status,
                        cudaStream_t st) {
-  return (int64_t)d.out * sizeof(T) % 16 == 0 ? launch<Cfg<BN, PAIR>, T, true>(x, w, bias, d, Y, status, st)
-                                              : launch<Cfg<BN, PAIR>, T, false>(x, w, bias, d, Y, status, st);
+  return (int64_t)d.out * sizeof(T) % 16 == 0 ? launch<C, T, true>(x, w, bias, d, Y, status, st)
+                                              : launch<C, T, false>(x, w, bias, d, Y, status, st);
 }
 
-template <typename T>
-cudaError_t launch_type(const Mx4View& x, const Mx4View& w, const void* bias, const Mx4Linear& d, void* Y, int* status,
-                        cudaStream_t st) {
-  if constexpr (sizeof(T) == 4) {
-    if (d.in > kRunFrom)
-      return d.out % 4 == 0 ? launch<Cfg<128, false, false, true>, float, true>(x, w, bias, d, Y, status, st)
-                            : launch<Cfg<128, false, false, true>, float, false>(x, w, bias, d, Y, status, st);
-  }
+// Which kernel a product takes (a Mx4Path).
+int choose(const Mx4Linear& d) {
+  if (d.dtype == MONARCH_F32 && d.in > kRunFrom) return kMx4Runs;
+  const int pitch = d.x().pitch();
   // The tile whose rounds over the SMs take the least time: a tile costs a stage's share of the way from
   // L2 for every 256 inputs, and its epilogue.  Microseconds from 8192 rows -> 4096 (256 x 256 pairs, 128 x 256
   // single, 128 x 256 with W kept): 19.8, 14.0 and 15.0 with 256 inputs, 22.5, 17.5 and 17.2 with 512, 26.9, 27.4 and
@@ -556,8 +552,8 @@ cudaError_t launch_type(const Mx4View& x, const Mx4View& w, const void* bias, co
     double stage, fixed;
   };
   const Tile tiles[4] = {{256, 256, 0.46, 2.3}, {128, 256, 0.62, 1.3}, {128, 128, 0.42, 1.0}, {128, 64, 0.30, 0.8}};
-  const double part = x.s.pitch() % 32 != 0 ? 1.2 : x.s.pitch() % 128 != 0 ? 0.33 : 0.0;  // for a short last stage
-  const int stages = (x.s.cols + 255) / 256;
+  const double part = pitch % 32 != 0 ? 1.2 : pitch % 128 != 0 ? 0.33 : 0.0;  // for a short last stage
+  const int stages = (d.in + 255) / 256;
   int best = 0;
   double least = 1e30;
   for (int i = 0; i < 4; ++i) {
@@ -573,20 +569,31 @@ cudaError_t launch_type(const Mx4View& x, const Mx4View& w, const void* bias, co
   // W kept: where its tiles are full ones, so that no CTA has a lighter one than the others, and every 32-byte
   // sector of Y has one writer (the CTAs of a row are at different rows: sixteen 90 -> 250 blocks 82 us, 64 without)
   const int64_t wtiles = (int64_t)d.nb * ((d.out + 255) / 256), share = num_sms() / wtiles;
-  if (stages <= 4 && share > 0 && d.out >= (d.out + 255) / 256 * 230 && (int64_t)d.out * sizeof(T) % 32 == 0) {
+  if (stages <= 4 && share > 0 && d.out >= (d.out + 255) / 256 * 230 && (int64_t)d.out * (d.dtype == MONARCH_BF16 ? 2 : 4) % 32 == 0) {
     const int64_t mtiles = (d.rows + 127) / 128, rounds = (mtiles + share - 1) / share;
-    if ((double)rounds * (stages * 0.33 + 1.6) + stages * 0.35 < least)
-      return launch<Cfg<256, false, true>, T, true>(x, w, bias, d, Y, status, st);
+    if ((double)rounds * (stages * 0.33 + 1.6) + stages * 0.35 < least) return kMx4Kept;
   }
-  switch (best) {
-    case 0: return launch_out<256, true, T>(x, w, bias, d, Y, status, st);
-    case 1: return launch_out<256, false, T>(x, w, bias, d, Y, status, st);
-    case 2: return launch_out<128, false, T>(x, w, bias, d, Y, status, st);
-    default: return launch_out<64, false, T>(x, w, bias, d, Y, status, st);
+  const int path[4] = {kMx4Pair, kMx4Tile256, kMx4Tile128, kMx4Tile64};
+  return path[best];
+}
+
+template <typename T>
+cudaError_t launch_type(const Mx4View& x, const Mx4View& w, const void* bias, const Mx4Linear& d, void* Y, int* status,
+                        cudaStream_t st) {
+  switch (choose(d)) {
+    case kMx4Pair: return launch_out<Cfg<256, true>, T>(x, w, bias, d, Y, status, st);
+    case kMx4Tile256: return launch_out<Cfg<256, false>, T>(x, w, bias, d, Y, status, st);
+    case kMx4Tile128: return launch_out<Cfg<128, false>, T>(x, w, bias, d, Y, status, st);
+    case kMx4Kept: return launch<Cfg<256, false, true>, T, true>(x, w, bias, d, Y, status, st);
+    case kMx4Runs:
+      if constexpr (sizeof(T) == 4) return launch_out<Cfg<128, false, false, true>, T>(x, w, bias, d, Y, status, st);
+    default: return launch_out<Cfg<64, false>, T>(x, w, bias, d, Y, status, st);
   }
 }
 
 }  // namespace
+
+int mx4_tc_path(const Mx4Linear& d) { return choose(d); }
 
 cudaError_t mx4_tc_fwd(const Mx4View& x, const Mx4View& w, const void* bias, const Mx4Linear& d, void* Y, int* status,
                        cudaStream_t st) {

@@ -19,7 +19,7 @@ import struct
 import torch
 
 from .build import native_key
-from . import MONARCH_BF16, MONARCH_F32, MonarchMx4Dims, MonarchMx4LinearDims, _check, dtype_code, lib
+from . import MONARCH_BF16, MONARCH_F32, MonarchMx4Dims, MonarchMx4LinearDims, _check, dtype_code, lib, make_dims
 
 _ENTRY_POINTS = ("monarch_mx4_code_bytes", "monarch_mx4_scale_bytes", "monarch_mx4_quantise", "monarch_mx4_dequantise",
                  "monarch_mx4_linear_wfwd_workspace_bytes", "monarch_mx4_linear_bwd_workspace_bytes", "monarch_mx4_linear_fwd",
@@ -167,6 +167,21 @@ def mx4_linear_workspace_bytes(rows: int, nblocks: int, in_blk: int, out_blk: in
     d = MonarchMx4LinearDims(int(rows), int(nblocks), int(in_blk), int(out_blk), int(bool(bias)), dtype_code(dtype))
     f = lib().monarch_mx4_linear_bwd_workspace_bytes if backward else lib().monarch_mx4_linear_wfwd_workspace_bytes
     return int(f(ctypes.byref(d)))
+
+
+_PRODUCTS = {"both": 0, "weights": 1, "dX": 2, "dW": 3}
+
+
+def mx4_linear_path(product: str, rows: int, nblocks: int, in_blk: int, out_blk: int, dtype="bf16") -> int:
+    """Kernels of one product of a layer (host-only query; `include/monarch.h` has the numbers): "both" operands in
+    MX4 or the "weights" alone (forward), "dX" or "dW"."""
+    d = MonarchMx4LinearDims(int(rows), int(nblocks), int(in_blk), int(out_blk), 0, dtype_code(dtype))
+    return lib().monarch_mx4_linear_path(ctypes.byref(d), _PRODUCTS[product])
+
+
+def mx4_fwd_path(shape: dict, rows: int, dtype="bf16") -> int:
+    """Kernels of mx4_fwd (host-only query): 0 the few-token ones, else fwd_path() of the forward behind the expanded factors."""
+    return lib().monarch_mx4_fwd_path(ctypes.byref(make_dims(shape, rows, dtype)))
 
 
 def mx4_linear_fwd(X, W: Mx4, bias=None, Y=None, dtype=None, workspace=None, stream=None):

@@ -387,6 +387,12 @@ typedef struct {
  * partial sums.  The forward needs none up to 64 bf16 or 32 fp32 rows, nor for more of a small weight. */
 MONARCH_API size_t monarch_mx4_linear_wfwd_workspace_bytes(const monarch_mx4_linear_dims* ld);
 MONARCH_API size_t monarch_mx4_linear_bwd_workspace_bytes(const monarch_mx4_linear_dims* ld);
+/* Kernels of a product (0: forward, both operands in MX4; 1: forward, W alone in MX4; 2: dX; 3: dW).  Host-only; -1 if ld
+ * or product is bad.  0, 1: few-token kernels (direct; shares of K on a cluster); 2 .. 7: block-scaled tensor-core
+ * product in tiles of 128 x 64, 128 x 128, 128 x 256, 128 x 256 with W's tile kept, 256 x 256 on CTA pairs, 128 x 128 in
+ * runs of K; 8, 9: bf16 product of the expanded operands in tiles of 128 x 128, 256 x 256 on CTA pairs, + 16 if K is
+ * split. */
+MONARCH_API int monarch_mx4_linear_path(const monarch_mx4_linear_dims* ld, int product);
 /* Both operands in MX4. */
 MONARCH_API int monarch_mx4_linear_fwd(const void* x_codes, const void* x_scales, const void* w_codes,
                                        const void* w_scales, const void* bias, const monarch_mx4_linear_dims* ld,
@@ -412,6 +418,8 @@ MONARCH_API int monarch_mx4_linear_bwd(const void* dY, const void* x_codes, cons
  * factors' values, with its rounding of the middle vector.
  * workspace: >= monarch_mx4_fwd_workspace_bytes(d), 256-byte aligned. */
 MONARCH_API size_t monarch_mx4_fwd_workspace_bytes(const monarch_dims* d);
+/* 0: the few-token kernels, else monarch_fwd_path of the forward behind the expanded factors; -1 if d is bad.  Host-only. */
+MONARCH_API int monarch_mx4_fwd_path(const monarch_dims* d);
 MONARCH_API int monarch_mx4_fwd(const void* X, const void* r_codes, const void* r_scales, const void* l_codes,
                                 const void* l_scales, const monarch_dims* d, void* Y, void* workspace,
                                 size_t workspace_bytes, void* stream);

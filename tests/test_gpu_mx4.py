@@ -704,3 +704,149 @@ def test_two_threads_on_their_own_streams():
         th.join()
     torch.cuda.synchronize()
     assert not faults and bdl.last_device_status() == 0
+
+
+# ---------------------------------------------------------------- every kernel by its path
+# Sizes for each kernel of a product, with the path they have to take: full and ragged tiles, fewer rows than a tile, result rows
+# that TMA can and cannot store, several tiles a CTA.  (product, rows, nblocks, in, out, dtype, path)
+PATHS = [
+    ("both", 777, 1, 96, 250, "bf16", 2), ("both", 33, 5, 200, 500, "bf16", 2), ("both", 127, 2, 96, 777, "f32", 2), ("both", 2000, 9, 300, 60, "f32", 2),
+    ("both", 1300, 5, 96, 130, "bf16", 3), ("both", 9, 5, 200, 2050, "bf16", 3), ("both", 127, 5, 200, 2000, "f32", 3),
+    ("both", 777, 3, 200, 500, "bf16", 3), ("both", 1300, 5, 96, 130, "f32", 3), ("both", 3000, 5, 700, 128, "bf16", 3),
+    ("both", 129, 5, 96, 2050, "bf16", 4), ("both", 520, 5, 96, 1000, "bf16", 4), ("both", 4000, 2, 96, 260, "f32", 4), ("both", 129, 5, 96, 2050, "f32", 4),
+    ("both", 9, 5, 96, 4096, "bf16", 5), ("both", 129, 5, 96, 2000, "f32", 5),
+    ("both", 2050, 5, 2048, 130, "bf16", 6), ("both", 3001, 1, 2000, 4001, "bf16", 6), ("both", 2500, 1, 4096, 2560, "bf16", 6), ("both", 2050, 5, 2048, 130, "f32", 6),
+    ("both", 2500, 1, 2090, 4000, "f32", 6), ("both", 257, 1, 16390, 200, "f32", 7), ("both", 200, 1, 20000, 1001, "f32", 7),
+    ("weights", 9, 5, 4096, 260, "bf16", 1), ("weights", 16, 1, 4096, 4096, "bf16", 1), ("weights", 31, 5, 520, 2000, "bf16", 1), ("weights", 64, 1, 4000, 1000, "bf16", 1),
+    ("weights", 50, 2, 2047, 2050, "bf16", 1), ("weights", 1, 1, 4096, 4096, "f32", 1), ("weights", 9, 1, 4095, 777, "f32", 1), ("weights", 32, 5, 520, 1000, "f32", 1),
+    ("weights", 257, 5, 96, 500, "bf16", 8), ("weights", 65, 5, 100, 2000, "bf16", 8), ("weights", 777, 2, 96, 250, "f32", 8), ("weights", 33, 5, 97, 2050, "f32", 8),
+    ("weights", 129, 5, 96, 2050, "bf16", 9), ("weights", 2000, 1, 1024, 4096, "bf16", 9), ("weights", 2001, 1, 1000, 4001, "bf16", 9),
+    ("weights", 129, 5, 96, 2050, "f32", 9), ("weights", 2001, 1, 1001, 4000, "f32", 9),
+    ("weights", 300, 1, 2048, 130, "bf16", 24), ("weights", 100, 5, 2048, 72, "bf16", 24), ("weights", 300, 2, 520, 130, "f32", 24), ("weights", 33, 1, 521, 2000, "f32", 24),
+    ("weights", 129, 5, 4096, 130, "bf16", 25), ("weights", 257, 1, 4096, 1000, "bf16", 25), ("weights", 129, 5, 1000, 130, "f32", 25), ("weights", 129, 1, 4096, 260, "f32", 25),
+    ("dX", 129, 5, 2048, 72, "bf16", 9), ("dX", 2500, 1, 1024, 4096, "bf16", 9), ("dX", 1500, 2, 1001, 2050, "bf16", 9), ("dX", 129, 5, 2048, 72, "f32", 9),
+    ("dX", 129, 1, 96, 2000, "bf16", 24), ("dX", 9, 1, 97, 2000, "bf16", 24), ("dX", 129, 1, 97, 500, "f32", 24),
+    ("dX", 129, 5, 200, 4096, "bf16", 25), ("dX", 129, 5, 201, 1000, "f32", 25),
+    ("dW", 129, 5, 2048, 130, "bf16", 9), ("dW", 2000, 1, 1024, 4000, "bf16", 9), ("dW", 1501, 2, 1000, 2050, "bf16", 9), ("dW", 9, 5, 2047, 130, "f32", 9),
+    ("dW", 1300, 1, 96, 72, "bf16", 24), ("dW", 520, 1, 97, 72, "f32", 24), ("dW", 4000, 5, 200, 130, "bf16", 25), ("dW", 2050, 1, 521, 130, "f32", 25),
+]
+
+
+def gpu_layer(rows, nb, inn, out, dtype, seed, x_by=1.0, w_by=1.0):
+    """Tensors of a layer made on the GPU, its quantised operands, and every operand's values in 64 bits there (roundings to
+    MX4 are compared with the oracle above, so a quantised operand's values are what it dequantises to)."""
+    g = torch.Generator(device="cuda").manual_seed(seed + 7 * rows + inn + out)
+    T = TORCH[dtype]
+
+    def normal(*shape):
+        return torch.randn(shape, generator=g, device="cuda")
+    t = {"X": (normal(rows, nb * inn) * x_by).to(T), "W": (normal(nb, out, inn) * w_by / inn ** 0.5).to(T),
+         "dY": normal(rows, nb * out).to(T), "b": normal(nb * out).to(T)}
+    Xq, Wq = bdl.mx4_quantise(t["X"], nblocks=nb), bdl.mx4_quantise(t["W"])
+    v = {k: t[k].double() for k in ("X", "dY", "b")}
+    v["Xq"], v["W"] = bdl.mx4_dequantise(Xq).double(), bdl.mx4_dequantise(Wq).double()
+    return t, Xq, Wq, v
+
+
+def gpu_product(product, v, nb, absolute=False):
+    v = {k: x.abs() for k, x in v.items()} if absolute else v
+    dy, w = v["dY"].view(len(v["dY"]), nb, -1).transpose(0, 1), v["W"]
+    x = v["X" if product == "weights" else "Xq"].view(len(v["X"]), nb, -1).transpose(0, 1)
+    if product in ("both", "weights"):
+        return (x @ w.transpose(1, 2)).transpose(0, 1).reshape(len(v["X"]), -1) + v["b"]
+    return (dy @ w).transpose(0, 1).reshape(len(v["X"]), -1) if product == "dX" else dy.transpose(1, 2) @ x
+
+
+def gpu_close(product, got, v, nb, terms, dtype):
+    ref, mags = gpu_product(product, v, nb), gpu_product(product, v, nb, True)
+    off = (got.double() - ref).abs() - (HALF[dtype] * ref.abs() + (terms * 2.0 ** -23) * mags + 2.0 ** -126)
+    assert got.shape == ref.shape and bool((off <= 0).all()), (product, int((~(off <= 0)).sum()), off.max())
+
+
+@pytest.mark.parametrize("product,rows,nb,inn,out,dtype,path", PATHS)
+def test_every_kernel(product, rows, nb, inn, out, dtype, path):
+    assert bdl.mx4_linear_path(product, rows, nb, inn, out, dtype) == path
+    t, Xq, Wq, v = gpu_layer(rows, nb, inn, out, dtype, 8)
+    if product in ("both", "weights"):
+        got, ok = guarded((rows, nb * out), TORCH[dtype])
+        bdl.mx4_linear_fwd(Xq if product == "both" else t["X"], Wq, bias=t["b"], Y=got)
+    else:
+        got, ok = guarded((rows, nb * inn) if product == "dX" else (nb, out, inn), TORCH[dtype])
+        bdl.mx4_linear_bwd(t["dY"], Xq if product == "dW" else None, Wq, need_dX=product == "dX", **{product: got})
+    gpu_close(product, got, v, nb, {"dX": out, "dW": rows}.get(product, inn) + 2, dtype)
+    assert ok() and bdl.last_device_status() == 0
+
+
+# a few-row call and a long one of the same layer, on every path of the two forwards that has no such test above
+@pytest.mark.parametrize("rows,nb,inn,out,both,weights", [
+    (16, 2, 1024, 4096, 2, 1), (900, 2, 600, 1024, 3, 8), (700, 2, 1024, 2050, 4, 9), (1500, 2, 600, 1024, 5, 9), (2100, 2, 2048, 1030, 6, 9)])
+def test_nan_and_infinity_stay_in_their_rows_on_every_path(rows, nb, inn, out, both, weights):
+    assert bdl.mx4_linear_path("both", rows, nb, inn, out) == both
+    assert bdl.mx4_linear_path("weights", rows, nb, inn, out) == weights
+    test_nan_and_infinity_stay_in_their_rows(rows, nb, inn, out)
+
+
+@pytest.mark.parametrize("rows,nb,inn,out,both,weights", [
+    (16, 1, 2048, 4096, 2, 1), (2100, 2, 2048, 1030, 6, 9), (1500, 2, 600, 1024, 5, 9), (777, 3, 200, 500, 3, 8), (1025, 1, 700, 4001, 4, 8)])
+def test_nothing_is_written_outside_the_outputs_on_every_path(rows, nb, inn, out, both, weights):
+    assert bdl.mx4_linear_path("both", rows, nb, inn, out) == both
+    assert bdl.mx4_linear_path("weights", rows, nb, inn, out) == weights
+    test_nothing_is_written_outside_the_outputs(rows, nb, inn, out)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,out,both", [(520, 1024, 2), (1300, 1024, 3), (3000, 1030, 4), (1300, 2000, 5), (3000, 4001, 6)])
+def test_extreme_scales_on_every_path(rows, out, both, dtype):
+    """Weights of 2^100 and 2^-100 against activations that bring the products back into range, in tensor-core tiles."""
+    inn = 2112 if both == 6 else 544
+    assert bdl.mx4_linear_path("both", rows, 1, inn, out, dtype) == both
+    up = torch.where(torch.arange(inn, device="cuda") // 32 % 2 == 0, 100.0, -90.0)
+    t, Xq, Wq, v = gpu_layer(rows, 1, inn, out, dtype, 9, torch.exp2(-up), torch.exp2(up))
+    dX, dW, _ = bdl.mx4_linear_bwd(t["dY"], Xq, Wq)
+    for product, got, terms in (("both", bdl.mx4_linear_fwd(Xq, Wq, bias=t["b"]), inn), ("weights", bdl.mx4_linear_fwd(t["X"], Wq, bias=t["b"]), inn),
+                                ("dX", dX, out), ("dW", dW, rows)):
+        gpu_close(product, got, v, 1, terms + 2, dtype)
+
+
+@pytest.mark.parametrize("rows,nb,inn,out,dtype", [(16, 1, 4096, 4096, "bf16"), (2100, 1, 2048, 1030, "bf16"), (900, 2, 1100, 1024, "f32")])
+def test_captured_graphs_of_long_layers(rows, nb, inn, out, dtype):
+    """Two graphs of a layer's step, with memory of their own, replayed at once on two streams and new inputs."""
+    def step(t, Wq):
+        Xq = bdl.mx4_quantise(t["X"], nblocks=nb)
+        return [bdl.mx4_linear_fwd(Xq, Wq, bias=t["b"]), bdl.mx4_linear_fwd(t["X"], Wq, bias=t["b"]),
+                *bdl.mx4_linear_bwd(t["dY"], Xq, Wq, bias=True)]
+    sets, graphs, outs = [], [], []
+    for k in range(2):
+        t = gpu_layer(rows, nb, inn, out, dtype, 40 + k)[0]
+        sets.append((t, bdl.mx4_quantise(t["W"])))
+        step(*sets[k])
+    torch.cuda.synchronize()
+    for s in sets:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(step(*s))
+        graphs.append(g)
+    for k, s in enumerate(sets):
+        n = gpu_layer(rows, nb, inn, out, dtype, 50 + k)[0]
+        for key in ("X", "dY", "b"):
+            s[0][key].copy_(n[key])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for s, o in zip(sets, outs):
+        assert all(torch.equal(a, b) for a, b in zip(o, step(*s)))
+    assert bdl.last_device_status() == 0
+
+
+@pytest.mark.parametrize("rows,nb1,in1,out1,nb2,in2,out2,tr,dtype,path", [
+    (3000, 32, 32, 32, 32, 32, 32, 1, "bf16", 2), (2000, 16, 48, 48, 48, 16, 64, 1, "bf16", 3), (700, 64, 64, 64, 64, 64, 64, 1, "bf16", 4),
+    (1500, 4, 256, 256, 4, 256, 1024, 0, "bf16", 1), (1500, 4, 256, 256, 4, 256, 256, 0, "bf16", 0), (3000, 32, 32, 32, 32, 32, 32, 1, "f32", 0),
+    (700, 64, 64, 64, 64, 64, 64, 1, "f32", 0), (70, 2, 1024, 1000, 2, 1000, 1024, 0, "bf16", 0), (70, 2, 1024, 1000, 2, 1000, 1024, 0, "f32", 0)])
+def test_monarch_forward_of_a_prompt(rows, nb1, in1, out1, nb2, in2, out2, tr, dtype, path):
+    shape = dict(nb1=nb1, in1=in1, out1=out1, nb2=nb2, in2=in2, out2=out2, out_transpose=tr)
+    assert bdl.mx4_fwd_path(shape, rows, dtype) == path and bdl.mx4_fwd_path(shape, 64, dtype) == 0
+    test_monarch_forward(rows, nb1, in1, out1, nb2, in2, out2, tr, dtype)

@@ -207,6 +207,25 @@ def test_monarch_rows_beyond_one_launch_keep_their_kernels(dtype):
     assert L.monarch_mx4_fwd_workspace_bytes(ctypes.byref(bdl.make_dims(shape, 100, dtype))) == 100 * 60000 * 4
 
 
+def test_path_queries():
+    from test_gpu_mx4 import PATHS
+    reached = {}
+    for product, rows, nb, inn, out, dtype, path in PATHS:
+        assert bdl.mx4_linear_path(product, rows, nb, inn, out, dtype) == path
+        reached.setdefault(product, set()).add(path)
+    # every kernel but the direct few-token one, which the small layers take
+    assert reached == {"both": {2, 3, 4, 5, 6, 7}, "weights": {1, 8, 9, 24, 25}, "dX": {9, 24, 25}, "dW": {9, 24, 25}}
+    assert bdl.mx4_linear_path("both", 1, 1, 64, 64) == bdl.mx4_linear_path("weights", 1, 1, 64, 64) == 0
+    assert bdl.mx4_linear_path("dX", 100, 1, 64, 64) == bdl.mx4_linear_path("dW", 100, 1, 64, 64) == 8
+    L = bdl.lib()
+    good, bad = bdl.MonarchMx4LinearDims(4, 1, 64, 64, 0, 0), bdl.MonarchMx4LinearDims(4, 0, 64, 64, 0, 0)
+    assert L.monarch_mx4_linear_path(None, 0) == L.monarch_mx4_linear_path(ctypes.byref(bad), 0) == -1
+    assert L.monarch_mx4_linear_path(ctypes.byref(good), 4) == L.monarch_mx4_linear_path(ctypes.byref(good), -1) == -1
+    shape = dict(nb1=32, in1=32, out1=32, nb2=32, in2=32, out2=32, out_transpose=1)
+    assert [bdl.mx4_fwd_path(shape, r, "bf16") for r in (1, 64, 5000)] == [0, 0, 2] and bdl.mx4_fwd_path(shape, 5000, "f32") == 0
+    assert bdl.mx4_fwd_path(dict(shape, in2=31), 5, "bf16") == L.monarch_mx4_fwd_path(None) == -1
+
+
 # ---------------------------------------------------------------- binding refusals (CPU tensors)
 def fake(rows, nb, cols, by_block, dtype="bf16"):
     d = bdl.MonarchMx4Dims(rows, nb, cols, int(by_block), bdl.dtype_code(dtype))
