@@ -169,7 +169,8 @@ cudaError_t fast_bwd(const void* dY, const void* X, const void* R, const void* L
     if (tc_stage_supported(s)) {
       // the permutations folded into the stages that produce Z and dU (tc_stage.cu)
       if (saved == nullptr) {
-        if ((e = tc_stage(X, R, Z, StageKind::R, s, status, st, true, true)) != cudaSuccess) return e;
+        // first in the call, it may follow a kernel that writes R and has let it start early
+        if ((e = tc_stage(X, R, Z, StageKind::R, s, status, st, true, prev)) != cudaSuccess) return e;
         prev = true;
       }
       if ((e = factor_transposes(R, Rt, L, Lt, s, 0, st, prev)) != cudaSuccess) return e;

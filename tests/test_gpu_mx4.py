@@ -548,6 +548,34 @@ def test_serving_chain_matches_its_parts():
         assert float((y - Y[r:r + 1]).float().norm()) <= 2.0 ** -6 * float(Y[r].float().norm())
 
 
+@pytest.mark.parametrize("tr", [0, 1])
+@pytest.mark.parametrize("blocks", [64, 32])
+def test_factors_that_a_product_has_just_written(blocks, tr):
+    """Monarch factors that are the result of the call before (a layer that makes another's weights): the maps that read
+    them wait for it.  New factors each time, so that old ones would show."""
+    n = blocks * blocks
+    shape = dict(nb1=blocks, in1=blocks, out1=blocks, nb2=blocks, in2=blocks, out2=blocks, out_transpose=tr)
+    g = torch.Generator(device="cuda").manual_seed(blocks)
+    Wq = bdl.mx4_quantise(torch.randn((1, n, 4096), generator=g, device="cuda").bfloat16() / 500)
+    X, dY = (torch.randn((500, n), generator=g, device="cuda").bfloat16() for _ in range(2))
+    R, L = (torch.empty((blocks, n), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    Xs = [torch.randn((blocks, 4096), generator=g, device="cuda").bfloat16() for _ in range(6)]
+
+    def run(k, wait):
+        bdl.mx4_linear_fwd(Xs[k], Wq, Y=L)
+        bdl.mx4_linear_fwd(Xs[k + 1], Wq, Y=R)
+        if wait:
+            torch.cuda.synchronize()
+        f = R.view(blocks, blocks, blocks), L.view(blocks, blocks, blocks)
+        if k % 2:
+            return [bdl.fwd(X, *f, shape), bdl.fwd_ws(X, *f, shape)]
+        return list(bdl.bwd(dY, X, *f, shape))
+    want = [run(k, True) for k in range(5)]
+    for _ in range(3):
+        for k in (0, 4, 1, 2, 3):
+            assert all(torch.equal(a, b) for a, b in zip(run(k, False), want[k])), k
+
+
 def guarded(shape, dtype):
     """A tensor inside a larger buffer filled with a pattern, and a check that the rest is untouched."""
     n = int(np.prod(shape))
