@@ -137,8 +137,8 @@ cudaError_t tc_wide_fwd_save(const void* X, const void* R, const void* L, void* 
 // Streaming block-diagonal stages with the row permutation folded into the stores (tc_stage.cu):
 //   R:  Z  = P blockdiag(R) X          L:  Y  = P_out blockdiag(L) Z
 //   Lt: dU = P^-1 blockdiag(L^T) dV     Rt: dX = blockdiag(R^T) dU
-// w_early: W may be read before the kernel's grid-dependency wait -- it is the caller's factor and another
-// kernel of the call has gone before (which waited for whatever the caller had written it with), or
+// w_early: W may be read before the kernel's grid-dependency wait -- it is the caller's factor and another kernel of
+// the call has gone before (which waited for whatever had written it) or the launch is in plain stream order (no pdl), or
 // it was written at least two launches earlier on the stream (that kernel has finished by then).
 enum class StageKind { R, L, Lt, Rt };
 bool tc_stage_supported(const Shape& s);

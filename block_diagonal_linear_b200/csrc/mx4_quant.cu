@@ -240,8 +240,7 @@ __global__ void __launch_bounds__(kQThreads)
     mx4_dequantise_kernel(Mx4View q, bool by_block, T* __restrict__ X, int64_t rtiles) {
   __shared__ __align__(16) uint8_t mem[PIECE == 32 ? 16 : sizeof(Tile<T>)];
   Tile<T>& tile = *(Tile<T>*)mem;
-  // No early start for the next kernel: the values may be a factor, which some forwards read ahead of their
-  // own grid-dependency wait.
+  // No early start for the next kernel: a map whose factor these values are would only wait.
   ptx::griddep_wait();
   const Mx4Shape& s = q.s;
   const int b = blockIdx.z, kq = threadIdx.x & 3, kb = blockIdx.y * 4 + kq, rr = threadIdx.x >> 2;

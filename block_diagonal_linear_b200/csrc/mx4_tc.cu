@@ -26,7 +26,7 @@
 // epilogue: two warps a TMEM lane quadrant, one row a thread, alternate 128-byte chunks of columns.  Each
 // warp stages and stores its own 32 rows, so that no warp waits for another (with four warps that met at
 // barriers around a common staging buffer the epilogue bounded short K: 10000 rows of four 256 -> 1024
-// blocks took 28.4 us, so 20.4).
+// blocks took 28.4 us, with these 20.4, and with the steps after them 17.0).
 #include "mx4.cuh"
 #include "tc_common.cuh"
 
