@@ -745,6 +745,7 @@ PATHS = [
     ("both", 9, 5, 96, 4096, "bf16", 5), ("both", 129, 5, 96, 2000, "f32", 5),
     ("both", 2050, 5, 2048, 130, "bf16", 6), ("both", 3001, 1, 2000, 4001, "bf16", 6), ("both", 2500, 1, 4096, 2560, "bf16", 6), ("both", 2050, 5, 2048, 130, "f32", 6),
     ("both", 2500, 1, 2090, 4000, "f32", 6), ("both", 257, 1, 16390, 200, "f32", 7), ("both", 200, 1, 20000, 1001, "f32", 7),
+    ("both", 9, 1, 16400, 4096, "f32", 7), ("both", 1300, 3, 16500, 1000, "f32", 7),
     ("weights", 9, 5, 4096, 260, "bf16", 1), ("weights", 16, 1, 4096, 4096, "bf16", 1), ("weights", 31, 5, 520, 2000, "bf16", 1), ("weights", 64, 1, 4000, 1000, "bf16", 1),
     ("weights", 50, 2, 2047, 2050, "bf16", 1), ("weights", 1, 1, 4096, 4096, "f32", 1), ("weights", 9, 1, 4095, 777, "f32", 1), ("weights", 32, 5, 520, 1000, "f32", 1),
     ("weights", 257, 5, 96, 500, "bf16", 8), ("weights", 65, 5, 100, 2000, "bf16", 8), ("weights", 777, 2, 96, 250, "f32", 8), ("weights", 33, 5, 97, 2050, "f32", 8),
